@@ -241,8 +241,9 @@ def _plain(s):
     start = s["h0"][..., None] if s["h0"] is not None else torch.zeros_like(h[..., :1])
     if kind == "train8":
         # the backward pass has the inputs as the checkpoint keeps them; the
-        # states at every 256th position are those of the forward pass
-        v, g = _through_8_bits(v), _through_8_bits(g)
+        # states at every 256th position are those of the forward pass; what
+        # lies behind a sequence's end counts as zero
+        v, g = _through_8_bits(_zero(v, live)), _through_8_bits(_zero(g, live))
         f, i, u = _gates(v, g, live)
         L = f.shape[-1]
         pad = -L % 256
@@ -391,6 +392,8 @@ def exact(case, seed):
                 step = _step64(part.abs().amax(dim=0))
                 out[t:t + SEQ_GROUP] = torch.round(part / step) * step
             return out
+        if on is not None:
+            v, g = torch.where(on, v, 0.0), torch.where(on, g, 0.0)
         v, g = kept(v), kept(g)
         f, i = torch.sigmoid(g), torch.sigmoid(-g)
         if on is not None:
