@@ -210,6 +210,139 @@ WBMM_API wbmm_status wbmm_backward_dt_static(const void *x, const void *dY, floa
                                              wbmm_dtype dt, void *stream);
 
 /*
+ * 8-bit activation checkpoints.  A group of values shares one power-of-two
+ * step 2^e; each value is kept as one unsigned byte:
+ *   a    = max |x| over the group
+ *   e    = the smallest exponent with rint(a / 2^e) <= 127, kept within
+ *          [-126, 121]
+ *   code = clamp(rint(x / 2^e), -127, 127) + 128       (ties to even)
+ *   exponent byte = e + 127                            (1..248)
+ * and stands for (code - 128) * 2^e, which bf16 and fp32 hold exactly, so
+ * storing a restored map again gives the same bytes.  |restored - x| is at
+ * most half a step, a/127 (a above 2^127 * 1.99 saturates to 127 steps).  A
+ * group that holds a NaN or an infinity has exponent byte 255 and codes 128
+ * and restores to NaN throughout, so an overflow in the forward pass is not
+ * hidden from the backward pass.
+ * Maps: a group is one w x w window of one channel.
+ *   codes [C][B*nh*nw][w*w] uint8, windows in (b, i, j) order (nh = H/w,
+ *         nw = W/w), positions u = p*w + q; B*C*H*W bytes, 16-byte aligned
+ *   exps  [C][B*nh*nw] uint8
+ * Sequences (wbmm_scan_forward): a group is WBMM_SEQ_GROUP successive
+ * positions of one row, the last one of a row shorter.
+ *   codes [B][C][L] uint8, 16-byte aligned
+ *   exps  [B][C][ceil(L / WBMM_SEQ_GROUP)] uint8
+ * The paper has no counterpart; a training step keeps x for the table
+ * gradient, and this form takes half (bf16) or a quarter (fp32) of its bytes.
+ */
+#define WBMM_SEQ_GROUP 64
+
+/*
+ * Stores a map in 8 bits.  x [B,C,H,W] dtype dt; codes, exps as above.
+ * Errors: as wbmm_forward.
+ */
+WBMM_API wbmm_status wbmm_checkpoint(const void *x, unsigned char *codes, unsigned char *exps,
+                                     int B, int C, int H, int W, int w, wbmm_dtype dt,
+                                     void *stream);
+
+/*
+ * Restores a map from its 8-bit form: x [B,C,H,W] dtype dt (overwritten).
+ * Errors: as wbmm_forward.
+ */
+WBMM_API wbmm_status wbmm_checkpoint_restore(const unsigned char *codes,
+                                             const unsigned char *exps, void *x, int B, int C,
+                                             int H, int W, int w, wbmm_dtype dt, void *stream);
+
+/*
+ * Bytes of device workspace wbmm_backward_checkpoint needs for the table
+ * gradient.  It starts with the arrival counters of
+ * wbmm_backward_workspace_bytes, under the same rules (zero before the first
+ * use, left zero by every call, shared with wbmm_backward's calls).  Returns
+ * 0 for invalid shapes.
+ */
+WBMM_API size_t wbmm_backward_checkpoint_workspace_bytes(int B, int C, int H, int W, int w,
+                                                         wbmm_dtype dt);
+
+/*
+ * wbmm_backward with the forward's input taken from its 8-bit checkpoint
+ * (codes and exps as wbmm_checkpoint writes them): dX is the same, dT is the
+ * table gradient of the restored map, bit for bit that of wbmm_backward on
+ * it.  codes and exps may be NULL when dT is NULL.
+ * Errors: as wbmm_backward.
+ */
+WBMM_API wbmm_status wbmm_backward_checkpoint(const unsigned char *codes,
+                                              const unsigned char *exps, const void *T,
+                                              const void *dY, void *dX, float *dT,
+                                              void *workspace, size_t ws_bytes, int B, int C,
+                                              int H, int W, int w, wbmm_dtype dt, void *stream);
+
+/*
+ * Gated linear recurrence along the positions of each (batch, channel) row,
+ * the mixer across windows with unbounded reach:
+ *   f_t = 1 / (1 + exp(-g_t)),   h_t = f_t h_{t-1} + (1 - f_t) v_t,   y_t = h_t
+ * for t = 0 .. L-1 with h_{-1} = h0 (zero when h0 is NULL).  A map
+ * [B,C,H,W] is L = H*W positions in row-major order.
+ *   v, g, y [B,C,L] dtype dt;  h0, hT [B,C] fp32, either NULL;
+ *   lengths [B] int32 or NULL: sequence b has min(max(lengths[b], 0), L)
+ *     positions; the later ones of v and g have no influence, y is zero
+ *     there, and hT is the state after the sequence's last position (h0 for
+ *     an empty one).
+ *   hT may be h0's own buffer (a state carried from call to call).
+ * For training:
+ *   states: fp32, wbmm_scan_states_bytes() bytes, or NULL; receives the
+ *     state before every 256th position, from which the backward pass
+ *     recomputes the others.  Entries behind a sequence's end are not written.
+ *   v_codes, v_exps, g_codes, g_exps: all four or none; receive 8-bit
+ *     checkpoints of v and g as sequences, positions behind a sequence's end
+ *     taken as zero.
+ * The state, the gates and all sums are fp32 for both dtypes; y is rounded
+ * once.  Results are bit-identical from run to run.
+ * Errors: INVALID_ARG (null pointer, B, C or L <= 0, overlap), DTYPE,
+ * ALIGNMENT, UNSUPPORTED (B*C >= 2^31), CUDA.
+ */
+WBMM_API wbmm_status wbmm_scan_forward(const void *v, const void *g, const float *h0,
+                                       const int *lengths, void *y, float *hT, float *states,
+                                       unsigned char *v_codes, unsigned char *v_exps,
+                                       unsigned char *g_codes, unsigned char *g_exps, int B,
+                                       int C, int L, wbmm_dtype dt, void *stream);
+
+/* Bytes of the states array, 4 * B * C * ceil(L / 256); 0 for invalid sizes. */
+WBMM_API size_t wbmm_scan_states_bytes(int B, int C, int L);
+
+/*
+ * Backward of wbmm_scan_forward.  With c_{L} = dhT (zero when NULL):
+ *   dh_t = dY_t + c_{t+1},   c_t = f_t dh_t,   dh0 = c_0,
+ *   dv_t = (1 - f_t) dh_t,   dg_t = f_t (1 - f_t) (h_{t-1} - v_t) dh_t
+ *   v, g, lengths, states: as given to and written by the forward call
+ *   dY, dv, dg [B,C,L] dtype dt (dv, dg overwritten; zero behind a
+ *     sequence's end, where dY is not used)
+ *   dhT, dh0 [B,C] fp32, either NULL (dh0 overwritten; it may be dhT's own
+ *     buffer)
+ * Errors: as wbmm_scan_forward.
+ */
+WBMM_API wbmm_status wbmm_scan_backward(const void *v, const void *g, const float *states,
+                                        const int *lengths, const void *dY, const float *dhT,
+                                        void *dv, void *dg, float *dh0, int B, int C, int L,
+                                        wbmm_dtype dt, void *stream);
+
+/*
+ * The same with v and g taken from the 8-bit checkpoints that the forward
+ * call wrote; the states at every 256th position are the forward's own.
+ */
+WBMM_API wbmm_status wbmm_scan_backward_checkpoint(
+    const unsigned char *v_codes, const unsigned char *v_exps, const unsigned char *g_codes,
+    const unsigned char *g_exps, const float *states, const int *lengths, const void *dY,
+    const float *dhT, void *dv, void *dg, float *dh0, int B, int C, int L, wbmm_dtype dt,
+    void *stream);
+
+/*
+ * One position of the recurrence for every row (serving): v, g, y [B,C]
+ * dtype dt, h, h_next [B,C] fp32; h_next may be h's own buffer.
+ * Errors: as wbmm_scan_forward.
+ */
+WBMM_API wbmm_status wbmm_scan_step(const void *v, const void *g, const float *h, void *y,
+                                    float *h_next, int B, int C, wbmm_dtype dt, void *stream);
+
+/*
  * Synchronises `stream`, then reports and clears the device status word that
  * kernels set when a bounded wait expires (WBMM_ERR_TIMEOUT), or returns
  * WBMM_ERR_CUDA for a sticky CUDA error.  WBMM_OK otherwise.

@@ -199,3 +199,126 @@ def test_static_table_gradient_argument_checks(lib):
     assert f(A0, A1, A0 + 64, 2, 4, 28, 28, 14, 1, None) == 1       # dT overlaps x
     # more partial tables than the 4 MiB static array holds
     assert f(A0, A1, A2, 1, 2048, 14, 14, 14, 1, None) == 6
+
+
+def test_checkpoint_argument_checks(lib):
+    st = _proto(lib, "wbmm_checkpoint", [P, P, P] + [I] * 6 + [P])
+    re_ = _proto(lib, "wbmm_checkpoint_restore", [P, P, P] + [I] * 6 + [P])
+    shape = (2, 4, 28, 28, 14)
+    assert st(A0, A1, A2, *shape, 2, None) == 3
+    assert st(None, A1, A2, *shape, 1, None) == 1
+    assert st(A0, None, A2, *shape, 1, None) == 1
+    assert st(A0, A1, None, *shape, 1, None) == 1
+    assert st(A0, A1, A2, 2, 4, 28, 29, 14, 1, None) == 2
+    assert st(A0, A1, A2, 0, 4, 28, 28, 14, 1, None) == 1
+    assert st(A0, A1, A2, 1, 4, 130, 130, 65, 1, None) == 5
+    assert st(A0 + 2, A1, A2, *shape, 1, None) == 4
+    assert st(A0, A1 + 8, A2, *shape, 1, None) == 4
+    assert st(A0, A0 + 16, A2, *shape, 1, None) == 1     # codes overlap x
+    assert st(A0, A1, A1 + 6271, *shape, 1, None) == 1   # exponents overlap the codes' last byte
+    assert st(A0, A1, A0, *shape, 1, None) == 1
+    assert re_(A0, A1, A2, *shape, 7, None) == 3
+    assert re_(A0, A1, None, *shape, 1, None) == 1
+    assert re_(A0 + 4, A1, A2, *shape, 1, None) == 4
+    assert re_(A0, A1, A2 + 4, *shape, 1, None) == 4
+    assert re_(A0, A1, A0 + 16, *shape, 1, None) == 1
+    assert re_(A0, A1, A2, 2, 4, 27, 28, 14, 1, None) == 2
+
+
+def test_backward_checkpoint_argument_checks(lib):
+    f = _proto(lib, "wbmm_backward_checkpoint", [P] * 7 + [S] + [I] * 6 + [P])
+    ws = lib.wbmm_backward_checkpoint_workspace_bytes
+    ws.restype, ws.argtypes = S, [I] * 6
+    need = ws(2, 4, 28, 28, 14, 1)
+    plain = lib.wbmm_backward_workspace_bytes
+    plain.restype, plain.argtypes = S, [I] * 6
+    assert need >= plain(2, 4, 28, 28, 14, 1) > 0
+    assert ws(1, 1, 14, 15, 7, 1) == 0 and ws(1, 1, 14, 14, 7, 3) == 0
+    exps = 0x60000000
+
+    def call(codes=A0, exps=exps, T=A1, dY=A2, dX=A3, dT=A4, work=A4 + 0x100000, nbytes=need,
+             shape=(2, 4, 28, 28, 14), dt=1):
+        return f(codes, exps, T, dY, dX, dT, work, nbytes, *shape, dt, None)
+
+    assert call(dt=2) == 3
+    assert call(dY=None) == 1
+    assert call(T=None) == 1
+    assert call(codes=None) == 1
+    assert call(exps=None) == 1
+    assert call(shape=(2, 4, 28, 30, 14)) == 2
+    assert call(shape=(2, 4, 28, 28, 0)) == 1
+    assert call(codes=A0 + 8) == 4
+    assert call(dX=A3 + 8) == 4
+    assert call(dT=A4 + 2) == 4
+    assert call(dX=A2 + 64) == 1
+    assert call(dX=A0 + 64) == 1                         # dX overlaps the codes
+    assert call(dT=exps) == 1                            # dT overlaps the exponents
+    assert call(work=None) == 6
+    assert call(nbytes=need - 4) == 6
+    assert call(work=A4 + 0x100008) == 4
+    assert call(work=A0 + 64) == 1
+    assert call(work=A4 + 64) == 1
+    assert call(dT=None, codes=None, exps=None, work=None, nbytes=0, dX=A3 + 8) == 4
+
+
+def test_recurrence_argument_checks(lib):
+    f = _proto(lib, "wbmm_scan_forward", [P] * 11 + [I] * 4 + [P])
+    A = [0x10000000 * k for k in range(1, 13)]
+
+    def fwd(v=A[0], g=A[1], h0=A[2], n=A[3], y=A[4], hT=A[5], st=A[6], vc=A[7], ve=A[8], gc=A[9], ge=A[10],
+            shape=(2, 4, 100), dt=1):
+        return f(v, g, h0, n, y, hT, st, vc, ve, gc, ge, *shape, dt, None)
+
+    assert fwd(dt=2) == 3
+    assert fwd(v=None) == 1 and fwd(g=None) == 1 and fwd(y=None) == 1
+    assert fwd(vc=None) == 1 and fwd(ve=None) == 1 and fwd(gc=None) == 1 and fwd(ge=None) == 1
+    for shape in ((0, 4, 100), (2, 0, 100), (2, 4, 0), (2, -1, 100)):
+        assert fwd(shape=shape) == 1
+    assert fwd(v=A[0] + 2) == 4 and fwd(y=A[4] + 8) == 4 and fwd(vc=A[7] + 4) == 4
+    assert fwd(h0=A[2] + 2) == 4 and fwd(n=A[3] + 1) == 4 and fwd(st=A[6] + 2) == 4 and fwd(hT=A[5] + 2) == 4
+    assert fwd(v=A[0] + 2, dt=0) == 4
+    assert fwd(shape=(1 << 16, 1 << 15, 1), v=1 << 40, g=1 << 41, y=1 << 42, h0=None, n=None, hT=None, st=None,
+               vc=None, ve=None, gc=None, ge=None) == 5
+    assert fwd(y=A[0] + 16) == 1 and fwd(y=A[1]) == 1
+    assert fwd(hT=A[2] + 4) == 1                          # in place only as a whole
+    assert fwd(st=A[5]) == 1 and fwd(vc=A[9]) == 1 and fwd(hT=A[3]) == 1 and fwd(ge=A[4] + 1599) == 1
+
+    b = _proto(lib, "wbmm_scan_backward", [P] * 9 + [I] * 4 + [P])
+
+    def bwd(v=A[0], g=A[1], st=A[2], n=A[3], dy=A[4], dhT=A[5], dv=A[6], dg=A[7], dh0=A[8], shape=(2, 4, 100), dt=1):
+        return b(v, g, st, n, dy, dhT, dv, dg, dh0, *shape, dt, None)
+
+    assert bwd(dt=5) == 3
+    for k in ("v", "g", "st", "dy", "dv", "dg"):
+        assert bwd(**{k: None}) == 1
+    assert bwd(shape=(2, 4, -3)) == 1
+    assert bwd(v=A[0] + 2) == 4 and bwd(dg=A[7] + 2) == 4 and bwd(dh0=A[8] + 2) == 4
+    assert bwd(dv=A[0]) == 1 and bwd(dv=A[4]) == 1 and bwd(dg=A[6]) == 1 and bwd(dh0=A[2]) == 1
+    assert bwd(dh0=A[5] + 4) == 1
+
+    c = _proto(lib, "wbmm_scan_backward_checkpoint", [P] * 11 + [I] * 4 + [P])
+
+    def bwd8(vc=A[0], ve=A[1], gc=A[2], ge=A[3], st=A[4], n=A[5], dy=A[6], dhT=A[7], dv=A[8], dg=A[9], dh0=A[10],
+             shape=(2, 4, 100), dt=1):
+        return c(vc, ve, gc, ge, st, n, dy, dhT, dv, dg, dh0, *shape, dt, None)
+
+    assert bwd8(dt=5) == 3
+    for k in ("vc", "ve", "gc", "ge", "st", "dy", "dv", "dg"):
+        assert bwd8(**{k: None}) == 1
+    assert bwd8(vc=A[0] + 8) == 4 and bwd8(gc=A[2] + 1) == 4
+    assert bwd8(dv=A[0]) == 1 and bwd8(dg=A[3]) == 1 and bwd8(dh0=A[1]) == 1
+
+    s = _proto(lib, "wbmm_scan_step", [P] * 5 + [I] * 3 + [P])
+    assert s(A[0], A[1], A[2], A[3], A[4], 2, 4, 3, None) == 3
+    assert s(A[0], A[1], None, A[3], A[4], 2, 4, 1, None) == 1
+    assert s(A[0], A[1], A[2], A[3], None, 2, 4, 1, None) == 1
+    assert s(A[0], A[1], A[2], A[3], A[4], 2, 0, 1, None) == 1
+    assert s(A[0] + 8, A[1], A[2], A[3], A[4], 2, 4, 1, None) == 4
+    assert s(A[0], A[1], A[2] + 2, A[3], A[4], 2, 4, 1, None) == 4
+    assert s(A[0], A[1], A[2], A[0], A[4], 2, 4, 1, None) == 1
+    assert s(A[0], A[1], A[2], A[3], A[2] + 8, 2, 4, 1, None) == 1
+
+    n = lib.wbmm_scan_states_bytes
+    n.restype, n.argtypes = S, [I] * 3
+    assert n(2, 3, 1) == 24 and n(2, 3, 256) == 24 and n(2, 3, 257) == 48 and n(1, 1, (1 << 31) - 1) == 4 << 23
+    assert n(0, 3, 1) == 0 and n(2, -3, 1) == 0 and n(2, 3, 0) == 0

@@ -100,3 +100,57 @@ def test_workspace_size_dtypes(wb):
     assert wb.wbmm_backward_workspace_bytes(2, 3, 28, 28, 14, torch.float32) > 0
     with pytest.raises(TypeError):
         wb.wbmm_backward_workspace_bytes(2, 3, 28, 28, 14, torch.float16)
+
+
+def test_checkpoint_buffers(wb):
+    x = maps()
+    codes, exps = torch.zeros(x.numel(), dtype=torch.uint8), torch.zeros(24, dtype=torch.uint8)
+    for f in (lambda c, e: wb.wbmm_checkpoint(x, c, e, 14), lambda c, e: wb.wbmm_checkpoint_restore(c, e, x, 14)):
+        assert status_of(f, codes, exps) == "passed"
+        assert status_of(f, codes[1:], exps) == 1
+        assert status_of(f, codes, exps[1:]) == 1
+        assert status_of(f, codes.to(torch.int8), exps) == 3
+        assert status_of(f, codes, exps.int()) == 3
+    T, dY, dX = torch.zeros((3, 729), dtype=BF), maps(), maps()
+    dT, ws = torch.zeros((3, 729)), torch.zeros(16)
+    assert status_of(wb.wbmm_backward_checkpoint, codes, exps, T, dY, dX, dT, ws, 14) == "passed"
+    assert status_of(wb.wbmm_backward_checkpoint, codes[1:], exps, T, dY, dX, dT, ws, 14) == 1
+    assert status_of(wb.wbmm_backward_checkpoint, codes, exps[1:], T, dY, dX, dT, ws, 14) == 1
+    assert status_of(wb.wbmm_backward_checkpoint, codes, exps, T[:2], dY, dX, dT, ws, 14) == 1
+    assert status_of(wb.wbmm_backward_checkpoint, codes, exps, T, dY, dX, dT.to(BF), ws, 14) == 3
+
+
+def test_recurrence_buffers(wb):
+    B, C, L = 2, 3, 300
+    x, u8 = torch.zeros((B, C, L), dtype=BF), torch.uint8
+    h, n = torch.zeros((B, C)), torch.zeros(B, dtype=torch.int32)
+    st, cd, ex = torch.zeros((B, C, 2)), torch.zeros((B, C, L), dtype=u8), torch.zeros((B, C, 5), dtype=u8)
+    good = dict(v=x, g=x, h0=h, lengths=n, y=x, hT=h, states=st, vc=cd, ve=ex, gc=cd, ge=ex)
+
+    def fwd(**k):
+        return status_of(wb.wbmm_scan_forward, *{**good, **k}.values())
+    assert fwd() == "passed" and fwd(h0=None, lengths=None, hT=None, states=None) == "passed"
+    assert fwd(g=x[:1]) == 1 and fwd(y=x[:, :1]) == 1 and fwd(h0=h[:1]) == 1 and fwd(hT=h[:, :2]) == 1
+    assert fwd(lengths=n[:1]) == 1 and fwd(states=st[:, :, :1]) == 1 and fwd(gc=cd[:1]) == 1 and fwd(ve=ex[:1]) == 1
+    assert fwd(g=x.float()) == 3 and fwd(h0=h.to(BF)) == 3 and fwd(lengths=n.long()) == 3 and fwd(vc=ex.int()) == 3
+    good2 = dict(v=x, g=x, states=st, lengths=n, dY=x, dhT=h, dv=x, dg=x, dh0=h)
+
+    def bwd(**k):
+        return status_of(wb.wbmm_scan_backward, *{**good2, **k}.values())
+    assert bwd() == "passed" and bwd(dhT=None, dh0=None, lengths=None) == "passed"
+    assert bwd(v=x[:1]) == 1 and bwd(dg=x[:1]) == 1 and bwd(states=st[:1]) == 1 and bwd(dh0=h[:1]) == 1
+    assert bwd(dv=x.float()) == 3 and bwd(dhT=h.double()) == 3
+    good3 = dict(vc=cd, ve=ex, gc=cd, ge=ex, states=st, lengths=n, dY=x, dhT=h, dv=x, dg=x, dh0=h)
+
+    def bwd8(**k):
+        return status_of(wb.wbmm_scan_backward_checkpoint, *{**good3, **k}.values())
+    assert bwd8() == "passed" and bwd8(vc=cd[:1]) == 1 and bwd8(ge=ex[:, :, :4]) == 1 and bwd8(vc=cd.int()) == 3
+    s = x[:, :, 0].contiguous()
+    assert status_of(wb.wbmm_scan_step, s, s, h, s, h) == "passed"
+    assert status_of(wb.wbmm_scan_step, s, s[:1], h, s, h) == 1
+    assert status_of(wb.wbmm_scan_step, s, s, h[:1], s, h) == 1
+    assert status_of(wb.wbmm_scan_step, s, s, h, s, h.double()) == 3
+    with pytest.raises(ValueError):
+        wb.wbmm_scan_step(x, x, h, x, h)
+    with pytest.raises(ValueError):
+        wb.scan_forward(x[0, 0], x[0, 0])

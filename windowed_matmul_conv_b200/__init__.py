@@ -14,11 +14,15 @@ runs in the library's CUDA kernels.  Importing this package fails loudly if
 the library has not been built (``python windowed_matmul_conv_b200/build.py``).
 
 The convenience functions ``forward``, ``backward``, ``cache_matrices``,
-``reparam_merge``, ``forward_cached`` and ``dw3x3`` allocate outputs with
-torch and call the entry points above.
+``reparam_merge``, ``forward_cached``, ``dw3x3``, ``checkpoint``,
+``checkpoint_restore``, ``backward_checkpoint``, ``scan_forward``,
+``scan_forward_train``, ``scan_backward`` and ``scan_step`` allocate outputs
+with torch and call the entry points above.
 """
 import ctypes
+import math
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -42,7 +46,12 @@ EXPORTS = ("wbmm_forward", "wbmm_backward_workspace_bytes", "wbmm_backward",
            "wbmm_cache_matrices", "wbmm_reparam_merge", "wbmm_forward_cached", "wbmm_dw3x3",
            "wbmm_get_device_status", "wbmm_status_string", "wbmm_set_wait_budget",
            "wbmm_wait_selftest", "wbmm_launch_count", "wbmm_last_path",
-           "wbmm_backward_dt_static", "wbmm_debug_set")
+           "wbmm_backward_dt_static", "wbmm_debug_set", "wbmm_checkpoint",
+           "wbmm_checkpoint_restore", "wbmm_backward_checkpoint_workspace_bytes",
+           "wbmm_backward_checkpoint", "wbmm_scan_forward", "wbmm_scan_states_bytes",
+           "wbmm_scan_backward", "wbmm_scan_backward_checkpoint", "wbmm_scan_step")
+# positions of a sequence that share one step in its 8-bit checkpoint
+WBMM_SEQ_GROUP = 64
 
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _lib.wbmm_forward.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
@@ -54,6 +63,17 @@ _lib.wbmm_reparam_merge.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _vp]
 _lib.wbmm_backward_dt_static.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
 _lib.wbmm_forward_cached.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
 _lib.wbmm_dw3x3.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]
+_lib.wbmm_checkpoint.argtypes = [_vp] * 3 + [_i] * 6 + [_vp]
+_lib.wbmm_checkpoint_restore.argtypes = [_vp] * 3 + [_i] * 6 + [_vp]
+_lib.wbmm_backward_checkpoint_workspace_bytes.argtypes = [_i] * 6
+_lib.wbmm_backward_checkpoint_workspace_bytes.restype = _sz
+_lib.wbmm_backward_checkpoint.argtypes = [_vp] * 7 + [_sz] + [_i] * 6 + [_vp]
+_lib.wbmm_scan_forward.argtypes = [_vp] * 11 + [_i] * 4 + [_vp]
+_lib.wbmm_scan_states_bytes.argtypes = [_i] * 3
+_lib.wbmm_scan_states_bytes.restype = _sz
+_lib.wbmm_scan_backward.argtypes = [_vp] * 9 + [_i] * 4 + [_vp]
+_lib.wbmm_scan_backward_checkpoint.argtypes = [_vp] * 11 + [_i] * 4 + [_vp]
+_lib.wbmm_scan_step.argtypes = [_vp] * 5 + [_i] * 3 + [_vp]
 _lib.wbmm_get_device_status.argtypes = [_vp]
 _lib.wbmm_status_string.argtypes = [_i]
 _lib.wbmm_status_string.restype = ctypes.c_char_p
@@ -66,7 +86,9 @@ _lib.wbmm_last_path.argtypes = []
 _lib.wbmm_debug_set.argtypes = [_i, _i]
 for _f in ("wbmm_forward", "wbmm_backward", "wbmm_backward_dt_static", "wbmm_cache_matrices",
            "wbmm_reparam_merge", "wbmm_forward_cached", "wbmm_dw3x3", "wbmm_get_device_status", "wbmm_wait_selftest", "wbmm_last_path",
-           "wbmm_debug_set"):
+           "wbmm_debug_set", "wbmm_checkpoint", "wbmm_checkpoint_restore",
+           "wbmm_backward_checkpoint", "wbmm_scan_forward", "wbmm_scan_backward",
+           "wbmm_scan_backward_checkpoint", "wbmm_scan_step"):
     getattr(_lib, _f).restype = _i
 
 
@@ -141,6 +163,28 @@ def _map_shape(x):
     return tuple(int(v) for v in x.shape)
 
 
+def _windows(B, C, H, W, w):
+    w = int(w)
+    return B * C * (H // w) * (W // w) if w > 0 else 0
+
+
+def _seq_shape(v):
+    if v.dim() < 2:
+        raise ValueError("recurrence tensors must be [B, C, L], [B, C, H, W] or [B, C]")
+    return int(v.shape[0]), int(v.shape[1]), math.prod(int(n) for n in v.shape[2:])
+
+
+def _need_seq(ref, B, C, L, h0, hT, lengths, states, codes=(), exps=()):
+    _need("state in", h0, B * C, ref, torch.float32)
+    _need("state out", hT, B * C, ref, torch.float32)
+    _need("lengths", lengths, B, ref, torch.int32)
+    _need("states", states, wbmm_scan_states_bytes(B, C, L) // 4, ref, torch.float32)
+    for t in codes:
+        _need("codes", t, B * C * L, ref, torch.uint8)
+    for t in exps:
+        _need("exps", t, B * C * -(-L // WBMM_SEQ_GROUP), ref, torch.uint8)
+
+
 # --------------------------------------------------------------- entry points
 
 def wbmm_forward(x, T, y, w, stream=None):
@@ -201,6 +245,95 @@ def wbmm_dw3x3(y, K, z, stream=None):
     _need("K", K, C * 9, y)
     _need("z", z, y.numel(), y)
     _check(_lib.wbmm_dw3x3(_p(y), _p(K), _p(z), B, C, H, W, _dt(y), _stream(stream, y)))
+
+
+def wbmm_checkpoint(x, codes, exps, w, stream=None):
+    B, C, H, W = _map_shape(x)
+    _need("codes", codes, x.numel(), x, torch.uint8)
+    _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
+    _check(_lib.wbmm_checkpoint(_p(x), _p(codes), _p(exps), B, C, H, W, int(w), _dt(x),
+                                _stream(stream, x)))
+
+
+def wbmm_checkpoint_restore(codes, exps, x, w, stream=None):
+    B, C, H, W = _map_shape(x)
+    _need("codes", codes, x.numel(), x, torch.uint8)
+    _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
+    _check(_lib.wbmm_checkpoint_restore(_p(codes), _p(exps), _p(x), B, C, H, W, int(w), _dt(x),
+                                        _stream(stream, x)))
+
+
+def wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dtype):
+    dt = _dt(torch.empty(0, dtype=dtype))
+    return int(_lib.wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, int(w), dt))
+
+
+def wbmm_backward_checkpoint(codes, exps, T, dY, dX, dT, workspace, w, stream=None):
+    B, C, H, W = _map_shape(dY)
+    _need("codes", codes, dY.numel(), dY, torch.uint8)
+    _need("exps", exps, _windows(B, C, H, W, w), dY, torch.uint8)
+    _need("T", T, C * _tsz(w), dY)
+    _need("dX", dX, dY.numel(), dY)
+    _need("dT", dT, C * _tsz(w), dY, torch.float32)
+    if workspace is not None and workspace.get_device() != dY.get_device():
+        raise WbmmError(WBMM_ERR_INVALID_ARG, "workspace is on %s, the map on %s"
+                        % (workspace.device, dY.device))
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.wbmm_backward_checkpoint(_p(codes), _p(exps), _p(T), _p(dY), _p(dX), _p(dT),
+                                         _p(workspace), ws_bytes, B, C, H, W, int(w), _dt(dY),
+                                         _stream(stream, dY)))
+
+
+def wbmm_scan_forward(v, g, h0, lengths, y, hT, states, v_codes, v_exps, g_codes, g_exps,
+                      stream=None):
+    """v, g, y: [B, C, L] or a map [B, C, H, W] (L = H*W); the rest may be None."""
+    B, C, L = _seq_shape(v)
+    n = v.numel()
+    _need("g", g, n, v)
+    _need("y", y, n, v)
+    _need_seq(v, B, C, L, h0=h0, hT=hT, lengths=lengths, states=states,
+              codes=(v_codes, g_codes), exps=(v_exps, g_exps))
+    _check(_lib.wbmm_scan_forward(_p(v), _p(g), _p(h0), _p(lengths), _p(y), _p(hT), _p(states),
+                                  _p(v_codes), _p(v_exps), _p(g_codes), _p(g_exps), B, C, L,
+                                  _dt(v), _stream(stream, v)))
+
+
+def wbmm_scan_states_bytes(B, C, L):
+    return int(_lib.wbmm_scan_states_bytes(int(B), int(C), int(L)))
+
+
+def wbmm_scan_backward(v, g, states, lengths, dY, dhT, dv, dg, dh0, stream=None):
+    B, C, L = _seq_shape(dY)
+    for name, t in (("v", v), ("g", g), ("dv", dv), ("dg", dg)):
+        _need(name, t, dY.numel(), dY)
+    _need_seq(dY, B, C, L, h0=dhT, hT=dh0, lengths=lengths, states=states)
+    _check(_lib.wbmm_scan_backward(_p(v), _p(g), _p(states), _p(lengths), _p(dY), _p(dhT), _p(dv),
+                                   _p(dg), _p(dh0), B, C, L, _dt(dY), _stream(stream, dY)))
+
+
+def wbmm_scan_backward_checkpoint(v_codes, v_exps, g_codes, g_exps, states, lengths, dY, dhT, dv,
+                                  dg, dh0, stream=None):
+    B, C, L = _seq_shape(dY)
+    for name, t in (("dv", dv), ("dg", dg)):
+        _need(name, t, dY.numel(), dY)
+    _need_seq(dY, B, C, L, h0=dhT, hT=dh0, lengths=lengths, states=states,
+              codes=(v_codes, g_codes), exps=(v_exps, g_exps))
+    _check(_lib.wbmm_scan_backward_checkpoint(
+        _p(v_codes), _p(v_exps), _p(g_codes), _p(g_exps), _p(states), _p(lengths), _p(dY),
+        _p(dhT), _p(dv), _p(dg), _p(dh0), B, C, L, _dt(dY), _stream(stream, dY)))
+
+
+def wbmm_scan_step(v, g, h, y, h_next, stream=None):
+    """v, g, y: [B, C]; h, h_next: [B, C] fp32 (may be one buffer)."""
+    B, C, L = _seq_shape(v)
+    if L != 1:
+        raise ValueError("a step takes one position: [B, C]")
+    _need("g", g, B * C, v)
+    _need("y", y, B * C, v)
+    _need("h", h, B * C, v, torch.float32)
+    _need("h_next", h_next, B * C, v, torch.float32)
+    _check(_lib.wbmm_scan_step(_p(v), _p(g), _p(h), _p(y), _p(h_next), B, C, _dt(v),
+                               _stream(stream, v)))
 
 
 def wbmm_get_device_status(stream=None):
@@ -291,3 +424,94 @@ def dw3x3(y, K, stream=None):
     z = torch.empty_like(y)
     wbmm_dw3x3(y, K, z, stream)
     return z
+
+
+def checkpoint(x, w, stream=None):
+    """8-bit form of a map: codes [C, B*nh*nw, w*w] and exponent bytes
+    [C, B*nh*nw], one power-of-two step per window."""
+    B, C, H, W = _map_shape(x)
+    n = _windows(B, C, H, W, w) // max(1, C)
+    codes = torch.empty((C, n, x.numel() // max(1, C * n)), dtype=torch.uint8, device=x.device)
+    exps = torch.empty((C, n), dtype=torch.uint8, device=x.device)
+    wbmm_checkpoint(x, codes, exps, w, stream)
+    return codes, exps
+
+
+def checkpoint_restore(codes, exps, shape, w, dtype, stream=None):
+    x = torch.empty(tuple(shape), dtype=dtype, device=codes.device)
+    wbmm_checkpoint_restore(codes, exps, x, w, stream)
+    return x
+
+
+def backward_checkpoint(codes, exps, T, dY, w, need_dx=True, need_dt=True, stream=None):
+    """backward() with the forward's input as checkpoint() keeps it."""
+    B, C, H, W = _map_shape(dY)
+    dX = torch.empty_like(dY) if need_dx else None
+    dT = torch.empty((C, (2 * w - 1) ** 2), dtype=torch.float32, device=dY.device) if need_dt else None
+    ws = None
+    if need_dt:
+        nbytes = wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dY.dtype)
+        ws = torch.empty(max(1, (nbytes + 3) // 4), dtype=torch.float32, device=dY.device)
+        ws[:WBMM_DT_COUNTER_WORDS].zero_()      # the arrival counters start at zero
+    wbmm_backward_checkpoint(codes, exps, T, dY, dX, dT, ws, w, stream)
+    return dX, dT
+
+
+class ScanSaved(NamedTuple):
+    """What scan_forward_train keeps for scan_backward: v and g themselves, or
+    their 8-bit codes with exponent bytes, and the states at every 256th
+    position."""
+    v: torch.Tensor
+    g: torch.Tensor
+    v_exps: Optional[torch.Tensor]
+    g_exps: Optional[torch.Tensor]
+    states: torch.Tensor
+    lengths: Optional[torch.Tensor]
+
+
+def scan_forward(v, g, h0=None, lengths=None, stream=None):
+    """y and the last state [B, C] fp32 of the gated recurrence over [B, C, L]."""
+    y = torch.empty_like(v)
+    hT = torch.empty(v.shape[:2], dtype=torch.float32, device=v.device)
+    wbmm_scan_forward(v, g, h0, lengths, y, hT, None, None, None, None, None, stream)
+    return y, hT
+
+
+def scan_forward_train(v, g, h0=None, lengths=None, checkpoint=False, stream=None):
+    """scan_forward that also returns what scan_backward needs; with
+    `checkpoint` v and g are kept in 8 bits."""
+    B, C, L = _seq_shape(v)
+
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=v.device)
+
+    y, hT = torch.empty_like(v), new((B, C), torch.float32)
+    states = new((B, C, wbmm_scan_states_bytes(B, C, L) // max(1, 4 * B * C)), torch.float32)
+    kept = [None] * 4
+    if checkpoint:
+        n = -(-L // WBMM_SEQ_GROUP)
+        kept = [new(s, torch.uint8) for s in ((B, C, L), (B, C, n), (B, C, L), (B, C, n))]
+    wbmm_scan_forward(v, g, h0, lengths, y, hT, states, *kept, stream)
+    if checkpoint:
+        return y, hT, ScanSaved(kept[0], kept[2], kept[1], kept[3], states, lengths)
+    return y, hT, ScanSaved(v, g, None, None, states, lengths)
+
+
+def scan_backward(saved, dY, dhT=None, stream=None):
+    """dv, dg and dh0 [B, C] fp32 from scan_forward_train's `saved`."""
+    dv, dg = torch.empty_like(dY), torch.empty_like(dY)
+    dh0 = torch.empty(dY.shape[:2], dtype=torch.float32, device=dY.device)
+    if saved.v_exps is None:
+        wbmm_scan_backward(saved.v, saved.g, saved.states, saved.lengths, dY, dhT, dv, dg, dh0,
+                           stream)
+    else:
+        wbmm_scan_backward_checkpoint(saved.v, saved.v_exps, saved.g, saved.g_exps, saved.states,
+                                      saved.lengths, dY, dhT, dv, dg, dh0, stream)
+    return dv, dg, dh0
+
+
+def scan_step(v, g, h, stream=None):
+    """One position for every row: y [B, C] and the next state [B, C] fp32."""
+    y, h_next = torch.empty_like(v), torch.empty_like(h)
+    wbmm_scan_step(v, g, h, y, h_next, stream)
+    return y, h_next

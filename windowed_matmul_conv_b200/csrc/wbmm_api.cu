@@ -96,6 +96,10 @@ bool aligned(const void* p, wbmm_dtype dt)
     return dt == WBMM_BF16 ? (a % 16 == 0) : (a % 4 == 0);
 }
 
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
 struct Span {
     const void* p;
     size_t bytes;
@@ -133,6 +137,138 @@ long long dt_workspace_floats(const Geom& g, wbmm_dtype dt)
     if (dt == WBMM_BF16 && tc_dt_supported(g))
         return tc_dt_workspace_floats(g);
     return WBMM_DT_COUNTER_WORDS + (long long)g.C * simt_dt_chunks(g) * g.tsz;
+}
+
+// Bytes of a map's 8-bit checkpoint.
+size_t code_bytes(const Geom& g) { return (size_t)g.B * g.C * g.H * g.W; }
+
+size_t exp_bytes(const Geom& g) { return (size_t)g.C * (size_t)g.bands * g.nw; }
+
+// Where wbmm_backward_checkpoint keeps the restored map in its workspace.
+size_t ckpt_map_offset(const Geom& g, wbmm_dtype dt)
+{
+    return ((size_t)dt_workspace_floats(g, dt) * 4 + 15) / 16 * 16;
+}
+
+long long scan_tiles(int L) { return ((long long)L + kScanTile - 1) / kScanTile; }
+
+// Bytes of a recurrence call's buffers.
+struct SeqSizes {
+    long long rows;
+    size_t map, state, states, codes, exps;
+    SeqSizes(int B, int C, int L, wbmm_dtype dt)
+    {
+        rows = (long long)B * C;
+        codes = (size_t)rows * L;
+        map = codes * elem_size(dt);
+        state = (size_t)rows * 4;
+        states = state * scan_tiles(L);
+        exps = (size_t)rows * ((L + (long long)WBMM_SEQ_GROUP - 1) / WBMM_SEQ_GROUP);
+    }
+};
+
+// True when an output overlaps an input or another output; `carry_in` and
+// `carry_out` (a state updated in place) may be one buffer.
+bool clash(const Span* in, int nin, const Span* out, int nout, const void* carry_in,
+           const void* carry_out)
+{
+    for (int o = 0; o < nout; ++o) {
+        for (int i = 0; i < nin; ++i)
+            if (overlap(in[i], out[o]) &&
+                !(in[i].p == carry_in && out[o].p == carry_out && carry_in == carry_out))
+                return true;
+        for (int q = 0; q < o; ++q)
+            if (overlap(out[q], out[o]))
+                return true;
+    }
+    return false;
+}
+
+// The launches of a backward call whose arguments have been checked; x is
+// used by the table gradient only.
+wbmm_status backward_run(const Geom& g, const void* x, const void* T, const void* dY, void* dX,
+                         float* dT, void* workspace, wbmm_dtype dt, const Launch& L)
+{
+    wbmm_status st = WBMM_OK;
+    const bool tc_dt = dT && dt == WBMM_BF16 && tc_dt_supported(g);
+    // Both gradients on tensor cores and enough tiles to fill the device: the
+    // two kernels run at the same time on disjoint SMs (2/5 for dX, the rest
+    // for dT, the measured balance at w = 14), each walking the channels in
+    // the same order, so the second read of each dY tile is served from L2
+    // and one kernel's ramp and tail overlap the other's steady state.  The
+    // dT kernel's grid (and so its fixed summation order) is a function of
+    // the shape and the SM count only.
+    Launch Lx = L, Lt = L;
+    if (dX && tc_dt && tc_toep_supported(g) && tc_dt_tiles(g) >= 2LL * L.num_sms &&
+        L.num_sms >= 5) {
+        Lx.num_sms = (2 * L.num_sms + 2) / 5;
+        Lt.num_sms = L.num_sms - Lx.num_sms;
+    }
+    if (dX) {
+        if (dt == WBMM_BF16 && tc_toep_supported(g)) {
+            st = from_cuda(tc_toep_launch(g, kTableFlip, dY, T, dX, Lx));
+            t_last_path = 1;
+        } else if (dt == WBMM_BF16 && tc_fwd_supported(g, false)) {
+            st = from_cuda(tc_fwd_launch(g, kTableFlip, dY, T, dX, nullptr, L));
+            t_last_path = 1;
+        } else if (dt == WBMM_BF16 && tc_big_supported(g)) {
+            st = from_cuda(tc_big_launch(g, kTableFlip, dY, T, dX, L));
+            t_last_path = 1;
+        } else {
+            st = from_cuda(simt_fwd_launch(g, kTableFlip, dt == WBMM_BF16, dY, T, dX, L));
+            t_last_path = 2;
+        }
+        if (st != WBMM_OK)
+            return st;
+    }
+    if (dT) {
+        float* part = static_cast<float*>(workspace);
+        if (tc_dt) {
+            // dX, when requested, was the launch just before this one (every
+            // library kernel signals its dependents only after its own wait)
+            const bool after_dx = dX != nullptr;
+            st = from_cuda(tc_dt_launch(g, x, dY, part, dT, after_dx, Lt));
+        } else {
+            float* chunks = part + WBMM_DT_COUNTER_WORDS;
+            st = from_cuda(simt_dt_launch(g, dt == WBMM_BF16, x, dY, chunks, L));
+            if (st != WBMM_OK)
+                return st;
+            st = from_cuda(dt_finalize_launch(g.C, g.tsz, simt_dt_chunks(g), chunks, dT, L));
+        }
+    }
+    return st;
+}
+
+// The part that both backward entry points of the recurrence share; A holds
+// v and g, plain or as codes, already checked.
+wbmm_status scan_backward_checked(ScanArgs A, const float* states, const int* lengths,
+                                  const void* dY, const float* dhT, void* dv, void* dg, float* dh0,
+                                  int B, int C, int L, wbmm_dtype dt, void* stream)
+{
+    if (!states || !dY || !dv || !dg || B <= 0 || C <= 0 || L <= 0)
+        return WBMM_ERR_INVALID_ARG;
+    if (!aligned(dY, dt) || !aligned(dv, dt) || !aligned(dg, dt) || !aligned4(states) ||
+        !aligned4(lengths) || !aligned4(dhT) || !aligned4(dh0))
+        return WBMM_ERR_ALIGNMENT;
+    const SeqSizes z(B, C, L, dt);
+    if (z.rows >= (1ll << 31))
+        return WBMM_ERR_UNSUPPORTED;
+    const Span in[] = {{A.v, z.map},          {A.g, z.map},         {A.v_codes, z.codes},
+                       {A.v_exps, z.exps},    {A.g_codes, z.codes}, {A.g_exps, z.exps},
+                       {states, z.states},    {lengths, (size_t)B * 4}, {dY, z.map},
+                       {dhT, z.state}};
+    const Span out[] = {{dv, z.map}, {dg, z.map}, {dh0, z.state}};
+    if (clash(in, 10, out, 3, dhT, dh0))
+        return WBMM_ERR_INVALID_ARG;
+    Launch Ln;
+    wbmm_status st = make_launch(stream, &Ln);
+    if (st != WBMM_OK)
+        return st;
+    A.states = const_cast<float*>(states);
+    A.lengths = lengths;
+    A.dy = dY; A.h0 = dhT; A.dv = dv; A.dg = dg; A.hT = dh0;
+    A.rows = z.rows; A.C = C; A.L = L;
+    return from_cuda(scan_backward_launch(A, dt == WBMM_BF16, Ln));
 }
 
 }  // namespace
@@ -281,53 +417,7 @@ wbmm_status wbmm_backward(const void* x, const void* T, const void* dY, void* dX
     Launch L;
     if ((st = make_launch(stream, &L)) != WBMM_OK)
         return st;
-    const bool tc_dt = dT && dt == WBMM_BF16 && tc_dt_supported(g);
-    // Both gradients on tensor cores and enough tiles to fill the device: the
-    // two kernels run at the same time on disjoint SMs (2/5 for dX, the rest
-    // for dT, the measured balance at w = 14), each walking the channels in
-    // the same order, so the second read of each dY tile is served from L2
-    // and one kernel's ramp and tail overlap the other's steady state.  The
-    // dT kernel's grid (and so its fixed summation order) is a function of
-    // the shape and the SM count only.
-    Launch Lx = L, Lt = L;
-    if (dX && tc_dt && tc_toep_supported(g) && tc_dt_tiles(g) >= 2LL * L.num_sms &&
-        L.num_sms >= 5) {
-        Lx.num_sms = (2 * L.num_sms + 2) / 5;
-        Lt.num_sms = L.num_sms - Lx.num_sms;
-    }
-    if (dX) {
-        if (dt == WBMM_BF16 && tc_toep_supported(g)) {
-            st = from_cuda(tc_toep_launch(g, kTableFlip, dY, T, dX, Lx));
-            t_last_path = 1;
-        } else if (dt == WBMM_BF16 && tc_fwd_supported(g, false)) {
-            st = from_cuda(tc_fwd_launch(g, kTableFlip, dY, T, dX, nullptr, L));
-            t_last_path = 1;
-        } else if (dt == WBMM_BF16 && tc_big_supported(g)) {
-            st = from_cuda(tc_big_launch(g, kTableFlip, dY, T, dX, L));
-            t_last_path = 1;
-        } else {
-            st = from_cuda(simt_fwd_launch(g, kTableFlip, dt == WBMM_BF16, dY, T, dX, L));
-            t_last_path = 2;
-        }
-        if (st != WBMM_OK)
-            return st;
-    }
-    if (dT) {
-        float* part = static_cast<float*>(workspace);
-        if (tc_dt) {
-            // dX, when requested, was the launch just before this one (every
-            // library kernel signals its dependents only after its own wait)
-            const bool after_dx = dX != nullptr;
-            st = from_cuda(tc_dt_launch(g, x, dY, part, dT, after_dx, Lt));
-        } else {
-            float* chunks = part + WBMM_DT_COUNTER_WORDS;
-            st = from_cuda(simt_dt_launch(g, dt == WBMM_BF16, x, dY, chunks, L));
-            if (st != WBMM_OK)
-                return st;
-            st = from_cuda(dt_finalize_launch(C, g.tsz, simt_dt_chunks(g), chunks, dT, L));
-        }
-    }
-    return st;
+    return backward_run(g, x, T, dY, dX, dT, workspace, dt, L);
 }
 
 wbmm_status wbmm_cache_matrices(const void* T, void* M, int C, int w, wbmm_dtype dt,
@@ -435,6 +525,209 @@ wbmm_status wbmm_dw3x3(const void* y, const void* K, void* z, int B, int C, int 
     if (st != WBMM_OK)
         return st;
     return from_cuda(dw3x3_launch(g, dt == WBMM_BF16, y, K, z, L));
+}
+
+wbmm_status wbmm_checkpoint(const void* x, unsigned char* codes, unsigned char* exps, int B, int C,
+                            int H, int W, int w, wbmm_dtype dt, void* stream)
+{
+    if (!dtype_ok(dt))
+        return WBMM_ERR_DTYPE;
+    if (!x || !codes || !exps)
+        return WBMM_ERR_INVALID_ARG;
+    wbmm_status st = check_map(B, C, H, W, w);
+    if (st != WBMM_OK)
+        return st;
+    if (!aligned(x, dt) || !aligned16(codes))
+        return WBMM_ERR_ALIGNMENT;
+    const Geom g = make_geom(B, C, H, W, w);
+    const Span cs{codes, code_bytes(g)}, es{exps, exp_bytes(g)}, xs{x, map_bytes(g, dt)};
+    if (overlap(cs, xs) || overlap(es, xs) || overlap(cs, es))
+        return WBMM_ERR_INVALID_ARG;
+    Launch L;
+    if ((st = make_launch(stream, &L)) != WBMM_OK)
+        return st;
+    return from_cuda(checkpoint_launch(g, dt == WBMM_BF16, x, codes, exps, L));
+}
+
+wbmm_status wbmm_checkpoint_restore(const unsigned char* codes, const unsigned char* exps, void* x,
+                                    int B, int C, int H, int W, int w, wbmm_dtype dt, void* stream)
+{
+    if (!dtype_ok(dt))
+        return WBMM_ERR_DTYPE;
+    if (!x || !codes || !exps)
+        return WBMM_ERR_INVALID_ARG;
+    wbmm_status st = check_map(B, C, H, W, w);
+    if (st != WBMM_OK)
+        return st;
+    if (!aligned(x, dt) || !aligned16(codes))
+        return WBMM_ERR_ALIGNMENT;
+    const Geom g = make_geom(B, C, H, W, w);
+    const Span xs{x, map_bytes(g, dt)};
+    if (overlap(xs, Span{codes, code_bytes(g)}) || overlap(xs, Span{exps, exp_bytes(g)}))
+        return WBMM_ERR_INVALID_ARG;
+    Launch L;
+    if ((st = make_launch(stream, &L)) != WBMM_OK)
+        return st;
+    return from_cuda(checkpoint_restore_launch(g, dt == WBMM_BF16, codes, exps, x, L));
+}
+
+size_t wbmm_backward_checkpoint_workspace_bytes(int B, int C, int H, int W, int w, wbmm_dtype dt)
+{
+    if (!dtype_ok(dt) || check_map(B, C, H, W, w) != WBMM_OK)
+        return 0;
+    const Geom g = make_geom(B, C, H, W, w);
+    return ckpt_map_offset(g, dt) + map_bytes(g, dt);
+}
+
+wbmm_status wbmm_backward_checkpoint(const unsigned char* codes, const unsigned char* exps,
+                                     const void* T, const void* dY, void* dX, float* dT,
+                                     void* workspace, size_t ws_bytes, int B, int C, int H, int W,
+                                     int w, wbmm_dtype dt, void* stream)
+{
+    if (!dtype_ok(dt))
+        return WBMM_ERR_DTYPE;
+    if (!dY || (dX && !T) || (dT && (!codes || !exps)))
+        return WBMM_ERR_INVALID_ARG;
+    wbmm_status st = check_map(B, C, H, W, w);
+    if (st != WBMM_OK)
+        return st;
+    if (!aligned(dY, dt) || (dX && (!aligned(dX, dt) || !aligned(T, dt))) ||
+        (dT && (!aligned16(codes) || reinterpret_cast<uintptr_t>(dT) % 4 != 0)))
+        return WBMM_ERR_ALIGNMENT;
+    const Geom g = make_geom(B, C, H, W, w);
+    const size_t mb = map_bytes(g, dt);
+    const Span cs{codes, dT ? code_bytes(g) : 0}, es{exps, dT ? exp_bytes(g) : 0};
+    const Span ys{dY, mb}, xs{dX, dX ? mb : 0}, ts{T, dX ? (size_t)C * g.tsz * elem_size(dt) : 0};
+    if (overlap(xs, ys) || overlap(xs, ts) || overlap(xs, cs) || overlap(xs, es))
+        return WBMM_ERR_INVALID_ARG;
+    if (dT) {
+        const size_t need = wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dt);
+        const Span ds{dT, (size_t)C * g.tsz * 4};
+        if (overlap(ds, ys) || overlap(ds, cs) || overlap(ds, es) || overlap(ds, xs) ||
+            overlap(ds, ts) || overlap(ds, Span{workspace, ws_bytes}))
+            return WBMM_ERR_INVALID_ARG;
+        if (!workspace || ws_bytes < need)
+            return WBMM_ERR_WORKSPACE;
+        if (!aligned16(workspace))
+            return WBMM_ERR_ALIGNMENT;
+        const Span wsp{workspace, need};
+        if (overlap(wsp, ys) || overlap(wsp, cs) || overlap(wsp, es) || overlap(wsp, xs) ||
+            overlap(wsp, ts))
+            return WBMM_ERR_INVALID_ARG;
+    }
+    Launch L;
+    if ((st = make_launch(stream, &L)) != WBMM_OK)
+        return st;
+    void* x = nullptr;
+    if (dT) {
+        x = static_cast<char*>(workspace) + ckpt_map_offset(g, dt);
+        st = from_cuda(checkpoint_restore_launch(g, dt == WBMM_BF16, codes, exps, x, L));
+        if (st != WBMM_OK)
+            return st;
+    }
+    return backward_run(g, x, T, dY, dX, dT, workspace, dt, L);
+}
+
+size_t wbmm_scan_states_bytes(int B, int C, int L)
+{
+    if (B <= 0 || C <= 0 || L <= 0)
+        return 0;
+    return 4 * (size_t)B * C * scan_tiles(L);
+}
+
+wbmm_status wbmm_scan_forward(const void* v, const void* g, const float* h0, const int* lengths,
+                              void* y, float* hT, float* states, unsigned char* v_codes,
+                              unsigned char* v_exps, unsigned char* g_codes, unsigned char* g_exps,
+                              int B, int C, int L, wbmm_dtype dt, void* stream)
+{
+    if (!dtype_ok(dt))
+        return WBMM_ERR_DTYPE;
+    const bool keep = v_codes != nullptr;
+    if (!v || !g || !y || B <= 0 || C <= 0 || L <= 0 || keep != (v_exps != nullptr) ||
+        keep != (g_codes != nullptr) || keep != (g_exps != nullptr))
+        return WBMM_ERR_INVALID_ARG;
+    if (!aligned(v, dt) || !aligned(g, dt) || !aligned(y, dt) || !aligned4(h0) ||
+        !aligned4(lengths) || !aligned4(hT) || !aligned4(states) || !aligned16(v_codes) ||
+        !aligned16(g_codes))
+        return WBMM_ERR_ALIGNMENT;
+    const SeqSizes z(B, C, L, dt);
+    if (z.rows >= (1ll << 31))
+        return WBMM_ERR_UNSUPPORTED;
+    const Span in[] = {{v, z.map}, {g, z.map}, {h0, z.state}, {lengths, (size_t)B * 4}};
+    const Span out[] = {{y, z.map},          {hT, z.state},       {states, z.states},
+                        {v_codes, z.codes},  {v_exps, z.exps},    {g_codes, z.codes},
+                        {g_exps, z.exps}};
+    if (clash(in, 4, out, 7, h0, hT))
+        return WBMM_ERR_INVALID_ARG;
+    Launch Ln;
+    wbmm_status st = make_launch(stream, &Ln);
+    if (st != WBMM_OK)
+        return st;
+    ScanArgs A = {};
+    A.v = v; A.g = g; A.h0 = h0; A.lengths = lengths;
+    A.y = y; A.hT = hT; A.states = states;
+    A.v_codes = v_codes; A.v_exps = v_exps; A.g_codes = g_codes; A.g_exps = g_exps;
+    A.rows = z.rows; A.C = C; A.L = L;
+    return from_cuda(scan_forward_launch(A, dt == WBMM_BF16, Ln));
+}
+
+wbmm_status wbmm_scan_backward(const void* v, const void* g, const float* states,
+                               const int* lengths, const void* dY, const float* dhT, void* dv,
+                               void* dg, float* dh0, int B, int C, int L, wbmm_dtype dt,
+                               void* stream)
+{
+    if (!dtype_ok(dt))
+        return WBMM_ERR_DTYPE;
+    if (!v || !g)
+        return WBMM_ERR_INVALID_ARG;
+    if (!aligned(v, dt) || !aligned(g, dt))
+        return WBMM_ERR_ALIGNMENT;
+    ScanArgs A = {};
+    A.v = v; A.g = g;
+    return scan_backward_checked(A, states, lengths, dY, dhT, dv, dg, dh0, B, C, L, dt, stream);
+}
+
+wbmm_status wbmm_scan_backward_checkpoint(const unsigned char* v_codes, const unsigned char* v_exps,
+                                          const unsigned char* g_codes, const unsigned char* g_exps,
+                                          const float* states, const int* lengths, const void* dY,
+                                          const float* dhT, void* dv, void* dg, float* dh0, int B,
+                                          int C, int L, wbmm_dtype dt, void* stream)
+{
+    if (!dtype_ok(dt))
+        return WBMM_ERR_DTYPE;
+    if (!v_codes || !v_exps || !g_codes || !g_exps)
+        return WBMM_ERR_INVALID_ARG;
+    if (!aligned16(v_codes) || !aligned16(g_codes))
+        return WBMM_ERR_ALIGNMENT;
+    ScanArgs A = {};
+    A.v_codes = const_cast<unsigned char*>(v_codes);
+    A.v_exps = const_cast<unsigned char*>(v_exps);
+    A.g_codes = const_cast<unsigned char*>(g_codes);
+    A.g_exps = const_cast<unsigned char*>(g_exps);
+    return scan_backward_checked(A, states, lengths, dY, dhT, dv, dg, dh0, B, C, L, dt, stream);
+}
+
+wbmm_status wbmm_scan_step(const void* v, const void* g, const float* h, void* y, float* h_next,
+                           int B, int C, wbmm_dtype dt, void* stream)
+{
+    if (!dtype_ok(dt))
+        return WBMM_ERR_DTYPE;
+    if (!v || !g || !h || !y || !h_next || B <= 0 || C <= 0)
+        return WBMM_ERR_INVALID_ARG;
+    if (!aligned(v, dt) || !aligned(g, dt) || !aligned(y, dt) || !aligned4(h) || !aligned4(h_next))
+        return WBMM_ERR_ALIGNMENT;
+    const SeqSizes z(B, C, 1, dt);
+    if (z.rows >= (1ll << 31))
+        return WBMM_ERR_UNSUPPORTED;
+    const Span in[] = {{v, z.map}, {g, z.map}, {h, z.state}};
+    const Span out[] = {{y, z.map}, {h_next, z.state}};
+    if (clash(in, 3, out, 2, h, h_next))
+        return WBMM_ERR_INVALID_ARG;
+    Launch L;
+    wbmm_status st = make_launch(stream, &L);
+    if (st != WBMM_OK)
+        return st;
+    return from_cuda(scan_step_launch(v, g, h, y, h_next, z.rows, dt == WBMM_BF16, L));
 }
 
 wbmm_status wbmm_get_device_status(void* stream)

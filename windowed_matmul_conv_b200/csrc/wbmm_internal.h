@@ -107,6 +107,32 @@ cudaError_t reparam_merge_launch(int C, int w, int k, bool is_bf16, const void* 
                                  const void* Tk, void* M, const Launch& L);
 cudaError_t dw3x3_launch(const Geom& g, bool is_bf16, const void* y, const void* K, void* z,
                          const Launch& L);
+// 8-bit checkpoints of maps, groups = windows (codes [C][windows][w*w]).
+cudaError_t checkpoint_launch(const Geom& g, bool is_bf16, const void* x, uint8_t* codes,
+                              uint8_t* exps, const Launch& L);
+cudaError_t checkpoint_restore_launch(const Geom& g, bool is_bf16, const uint8_t* codes,
+                                      const uint8_t* exps, void* x, const Launch& L);
+
+// Gated linear recurrence.  Positions per entry of the states array, and per
+// group of a sequence's checkpoint.
+constexpr int kScanTile = 256;
+struct ScanArgs {
+    const void *v, *g;                          // dtype maps, or null with codes in the backward
+    uint8_t *v_codes, *v_exps, *g_codes, *g_exps;   // written forward, read backward; or null
+    const float* h0;                            // forward: first state; backward: dhT
+    const int* lengths;
+    float* states;
+    void* y;                                    // forward
+    float* hT;                                  // forward: last state; backward: dh0
+    const void* dy;                             // backward
+    void *dv, *dg;
+    long long rows;                             // B * C
+    int C, L;
+};
+cudaError_t scan_forward_launch(const ScanArgs& A, bool is_bf16, const Launch& L);
+cudaError_t scan_backward_launch(const ScanArgs& A, bool is_bf16, const Launch& L);
+cudaError_t scan_step_launch(const void* v, const void* g, const float* h, void* y, float* h_next,
+                             long long rows, bool is_bf16, const Launch& L);
 cudaError_t wait_selftest_launch(unsigned long long cycles, const Launch& L);
 
 void note_launches(int n);
