@@ -14,7 +14,8 @@ TILE = 256      # positions per kept state
 def group_step(top):
     """The smallest e, -126 <= e <= 121, with rint(top / 2^e) <= 127."""
     top = np.asarray(top, dtype=np.float64)
-    e = np.clip(np.frexp(top)[1] - 9, -126, 121)    # top / 2^e at least 256 where not at an end
+    # top / 2^e is at least 256 where e is not at an end (frexp gives 0 for 0)
+    e = np.where(top > 0, np.clip(np.frexp(top)[1] - 9, -126, 121), -126)
     while True:
         more = (e < 121) & (np.rint(np.ldexp(top, -e)) > 127)
         if not more.any():
