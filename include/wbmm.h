@@ -297,7 +297,7 @@ WBMM_API wbmm_status wbmm_backward_checkpoint(const unsigned char *codes,
  * The state, the gates and all sums are fp32 for both dtypes; y is rounded
  * once.  Results are bit-identical from run to run.
  * Errors: INVALID_ARG (null pointer, B, C or L <= 0, overlap), DTYPE,
- * ALIGNMENT, UNSUPPORTED (B*C >= 2^31), CUDA.
+ * ALIGNMENT, UNSUPPORTED (B*C >= 2^31 or L >= 2^31 - 65536), CUDA.
  */
 WBMM_API wbmm_status wbmm_scan_forward(const void *v, const void *g, const float *h0,
                                        const int *lengths, void *y, float *hT, float *states,

@@ -279,6 +279,8 @@ def test_recurrence_argument_checks(lib):
     assert fwd(v=A[0] + 2, dt=0) == 4
     assert fwd(shape=(1 << 16, 1 << 15, 1), v=1 << 40, g=1 << 41, y=1 << 42, h0=None, n=None, hT=None, st=None,
                vc=None, ve=None, gc=None, ge=None) == 5
+    assert fwd(shape=(1, 1, (1 << 31) - 65536), v=1 << 40, g=1 << 41, y=1 << 42, h0=None, n=None, hT=None, st=None,
+               vc=None, ve=None, gc=None, ge=None) == 5
     assert fwd(y=A[0] + 16) == 1 and fwd(y=A[1]) == 1
     assert fwd(hT=A[2] + 4) == 1                          # in place only as a whole
     assert fwd(st=A[5]) == 1 and fwd(vc=A[9]) == 1 and fwd(hT=A[3]) == 1 and fwd(ge=A[4] + 1599) == 1

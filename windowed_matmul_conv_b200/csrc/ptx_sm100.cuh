@@ -129,6 +129,14 @@ __device__ __forceinline__ void cp_async_4(uint32_t smem_dst, const void *gsrc)
                  : "memory");
 }
 
+// The same reading src_bytes (0 to 4) and zero-filling the rest.
+__device__ __forceinline__ void cp_async_4z(uint32_t smem_dst, const void *gsrc, uint32_t src_bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(gsrc),
+                 "r"(src_bytes)
+                 : "memory");
+}
+
 // Global -> shared copy of 8 bytes, both addresses 8-byte aligned.
 __device__ __forceinline__ void cp_async_8(uint32_t smem_dst, const void *gsrc)
 {
@@ -142,7 +150,7 @@ __device__ __forceinline__ void cp_async_wait_all()
 }
 
 // Global -> shared copy of 16 bytes (both addresses 16-byte aligned) that
-// reads src_bytes (0 or 16) from gsrc and zero-fills the rest; one commit
+// reads src_bytes (0 to 16) from gsrc and zero-fills the rest; one commit
 // group per call of cp_async_commit, completed in order.
 __device__ __forceinline__ void cp_async_16z(uint32_t smem_dst, const void *gsrc, uint32_t src_bytes)
 {
@@ -242,6 +250,41 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads)
 __device__ __forceinline__ void named_bar_arrive(int id, int nthreads)
 {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// ------------------------------------------------- thread-block clusters
+__device__ __forceinline__ uint32_t cluster_ctarank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Hardware barrier of every thread of the cluster; shared-memory writes
+// before it, remote ones included, are visible after it.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Writes two floats at this CTA's shared address `saddr` as seen in CTA
+// `rank` of the cluster.
+__device__ __forceinline__ void st_cluster_f2(uint32_t saddr, uint32_t rank, float a, float b)
+{
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %0, %1;\n\t"
+        "st.shared::cluster.v2.f32 [r], {%2, %3};\n\t}" ::"r"(saddr),
+        "r"(rank), "f"(a), "f"(b)
+        : "memory");
 }
 
 // ----------------------------------------------------------------- TMEM

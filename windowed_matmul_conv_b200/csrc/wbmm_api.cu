@@ -165,6 +165,9 @@ struct SeqSizes {
         states = state * scan_tiles(L);
         exps = (size_t)rows * ((L + (long long)WBMM_SEQ_GROUP - 1) / WBMM_SEQ_GROUP);
     }
+    // The kernels count a row's positions in 32 bits, up to some rounds of 32
+    // tiles past its end.
+    bool supported(int L) const { return rows < (1ll << 31) && L <= 0x7fffffff - 65536; }
 };
 
 // True when an output overlaps an input or another output; `carry_in` and
@@ -251,7 +254,7 @@ wbmm_status scan_backward_checked(ScanArgs A, const float* states, const int* le
         !aligned4(lengths) || !aligned4(dhT) || !aligned4(dh0))
         return WBMM_ERR_ALIGNMENT;
     const SeqSizes z(B, C, L, dt);
-    if (z.rows >= (1ll << 31))
+    if (!z.supported(L))
         return WBMM_ERR_UNSUPPORTED;
     const Span in[] = {{A.v, z.map},          {A.g, z.map},         {A.v_codes, z.codes},
                        {A.v_exps, z.exps},    {A.g_codes, z.codes}, {A.g_exps, z.exps},
@@ -651,7 +654,7 @@ wbmm_status wbmm_scan_forward(const void* v, const void* g, const float* h0, con
         !aligned16(g_codes))
         return WBMM_ERR_ALIGNMENT;
     const SeqSizes z(B, C, L, dt);
-    if (z.rows >= (1ll << 31))
+    if (!z.supported(L))
         return WBMM_ERR_UNSUPPORTED;
     const Span in[] = {{v, z.map}, {g, z.map}, {h0, z.state}, {lengths, (size_t)B * 4}};
     const Span out[] = {{y, z.map},          {hT, z.state},       {states, z.states},
@@ -717,7 +720,7 @@ wbmm_status wbmm_scan_step(const void* v, const void* g, const float* h, void* y
     if (!aligned(v, dt) || !aligned(g, dt) || !aligned(y, dt) || !aligned4(h) || !aligned4(h_next))
         return WBMM_ERR_ALIGNMENT;
     const SeqSizes z(B, C, 1, dt);
-    if (z.rows >= (1ll << 31))
+    if (!z.supported(1))
         return WBMM_ERR_UNSUPPORTED;
     const Span in[] = {{v, z.map}, {g, z.map}, {h, z.state}};
     const Span out[] = {{y, z.map}, {h_next, z.state}};

@@ -7,16 +7,22 @@
 // successive positions of one row, 8 a lane: each lane composes its 8 steps,
 // the lanes' maps are joined by an inclusive scan in 5 exchanges, and each
 // lane replays its 8 steps from its exact starting state.  The order of every
-// product and sum is fixed by the position within the row, so results are
-// bit-identical from run to run.
+// product and sum is fixed by the position within the row and the call's
+// sizes, so results are bit-identical from run to run.
 //
 // The backward pass needs h_{t-1}: it replays a tile from the state before it,
 // which the forward call keeps (one fp32 value per 256 positions), beside the
 // reversed recurrence of c_t = f_t (dy_t + c_{t+1}).
 //
 // 1 - f is e f with e = exp(-g), not a difference, so that it keeps its
-// relative accuracy where f is close to 1; exp's argument is held at 80 at
-// most, where f (1.8e-35) is zero for every purpose and e f is 1.
+// relative accuracy where f is close to 1; -g is held at about 79.6 at most,
+// where f (3e-35) is zero for every purpose and e f is 1.
+//
+// The bytes of a call (6 an element forward, 10 backward, in bf16) take the
+// memory 0.15 ns an element; the arithmetic is about 13 and 22 instructions an
+// element, half to two thirds of the issue slots in that time, so the code
+// around it is kept short: paired fp32 instructions (f32x2), one test a tile
+// for a partial tile, states and exponent bytes fetched for 32 tiles at once.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -32,6 +38,39 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 
+// ------------------------------------------------------------ pairs of fp32
+struct F2 {
+    float x, y;
+};
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 d)
+{
+    F2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mov.b64 d, {%6, %7};\n\tfma.rn.f32x2 c, a, b, d;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(d.x), "f"(d.y));
+    return r;
+}
+
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
@@ -44,21 +83,58 @@ __device__ __forceinline__ float min_nan(float a, float b)
     return r;
 }
 
-// f = sigmoid(g), i = 1 - f.
-template <typename T>
-__device__ __forceinline__ void gate(float g, float& f, float& i)
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    const float a = min_nan(-g, 80.0f);
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float ex2_fast(float a)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_fast(float a)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kGateMin = -79.5f;      // exact in bf16
+
+// f = 1 / (1 + e), i = 1 - f = e f with e = exp(-g) = 2^(-g log2 e), for two
+// gates.  ex2 is within 2^-22 and rcp within an ulp.  The rounding of the
+// product t and of the constant leave an error of 1.5 |g| 2^-24 in e, far
+// below bf16's 2^-8; fp32 maps take it back with the product's exact remainder
+// and the constant's next bits, 2^(t + r) = 2^t (1 + r ln 2), |r| < 2^-15.
+// bf16 gates have been held at kGateMin (in pairs, before they were widened),
+// fp32 ones are held at t = 115; neither these nor an infinite t has a
+// remainder.
+template <typename T>
+__device__ __forceinline__ void gate2(F2 g, F2& f, F2& i)
+{
+    F2 t = mul2(g, {-kLog2e, -kLog2e}), e;
     if constexpr (std::is_same<T, float>::value) {
-        const float e = expf(a);
-        f = __frcp_rn(1.0f + e);
-        i = e * f;
+        F2 r = fma2(g, {-kLog2e, -kLog2e}, {-t.x, -t.y});
+        r = mul2(fma2(g, {-kLog2eLow, -kLog2eLow}, r), {kLn2, kLn2});
+        t = {min_nan(t.x, 115.0f), min_nan(t.y, 115.0f)};
+        e = {ex2_fast(t.x), ex2_fast(t.y)};
+        const F2 c = fma2(e, r, e);
+        e.x = fabsf(t.x) < 115.0f ? c.x : e.x;
+        e.y = fabsf(t.y) < 115.0f ? c.y : e.y;
     } else {
-        // the fast forms' errors, about 2^-21, are far below bf16's 2^-8
-        const float e = __expf(a);
-        f = __fdividef(1.0f, 1.0f + e);
-        i = e * f;
+        e = {ex2_fast(t.x), ex2_fast(t.y)};
     }
+    const F2 d = add2(e, {1.0f, 1.0f});
+    f = {rcp_fast(d.x), rcp_fast(d.y)};
+    i = mul2(e, f);
 }
 
 // Positions of row b*C + c that the sequence has.
@@ -70,155 +146,148 @@ __device__ __forceinline__ int row_len(const int* lengths, long long row, int C,
     return n < 0 ? 0 : n > L ? L : n;
 }
 
-__device__ __forceinline__ int clamp8(long long n) { return n < 0 ? 0 : n > 8 ? 8 : (int)n; }
-
-// Eight successive elements as they sit in memory.  VEC: rows start at
-// 16-byte boundaries and hold a multiple of 8 elements, so a lane's elements
-// are whole 16-byte vectors.  Otherwise a lane takes 4-byte words (of a bf16
-// row that starts at an odd element: 4 words from the element before, which
-// belongs to the tensor, and the last element by itself), which costs no
-// shuffles; the words of neighbouring lanes share their sectors.
+// ------------------------------------------------------- eight of a lane's values
+// A lane's eight elements as they sit in memory.
 template <typename T>
 struct Raw {
     static constexpr int N = 2 * (int)sizeof(T);    // 32-bit words
     uint32_t w[N];
 };
 
-template <bool VEC, typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p, int cnt)
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw<T>& r, F2 (&x)[4])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4)
+            x[j] = {__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1])};
+        else
+            x[j] = {__uint_as_float(r.w[j] << 16), __uint_as_float(r.w[j] & 0xffff0000u)};
+    }
+}
+
+// The gates' arguments: as unpack8, bf16 ones held at kGateMin (NaN stays).
+template <typename T>
+__device__ __forceinline__ void unpack_gates8(const Raw<T>& r, F2 (&x)[4])
+{
+    if constexpr (sizeof(T) == 4) {
+        unpack8(r, x);
+    } else {
+        Raw<T> h;
+        constexpr uint32_t lim = 0xc29fc29fu;   // kGateMin twice
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(h.w[j]) : "r"(r.w[j]), "r"(lim));
+        unpack8(h, x);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Raw<T> pack8(const F2 (&x)[4])
 {
     Raw<T> r;
 #pragma unroll
-    for (int k = 0; k < Raw<T>::N; ++k)
-        r.w[k] = 0u;
-    if constexpr (VEC) {
-        if (cnt > 0) {
-#pragma unroll
-            for (int k = 0; k < Raw<T>::N; k += 4) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + k / 4);
-                r.w[k] = q.x; r.w[k + 1] = q.y; r.w[k + 2] = q.z; r.w[k + 3] = q.w;
-            }
-        }
-    } else if constexpr (sizeof(T) == 4) {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < cnt)
-                r.w[k] = __ldg(q + k);
-    } else if (cnt == 8) {
-        if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                r.w[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + k);
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+            r.w[2 * j] = __float_as_uint(x[j].x);
+            r.w[2 * j + 1] = __float_as_uint(x[j].y);
         } else {
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(p - 1);
-            uint32_t u[5];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                u[k] = __ldg(q + k);
-            u[4] = __ldg(reinterpret_cast<const unsigned short*>(p) + 7);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                r.w[k] = __funnelshift_r(u[k], u[k + 1], 16);
+            const __nv_bfloat162 q = __floats2bfloat162_rn(x[j].x, x[j].y);
+            r.w[j] = reinterpret_cast<const uint32_t&>(q);
         }
-    } else {
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < cnt)
-                r.w[k / 2] |= (uint32_t)__ldg(q + k) << (16 * (k & 1));
     }
     return r;
 }
 
-// As floats, zeros from cnt on.
+// Replaces the values from position cnt on.
+__device__ __forceinline__ void cut8(F2 (&x)[4], int cnt, float with)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j].x = 2 * j < cnt ? x[j].x : with;
+        x[j].y = 2 * j + 1 < cnt ? x[j].y : with;
+    }
+}
+
+// Eight codes and their group's exponent byte.
+struct RawCodes {
+    uint2 w;
+    uint32_t e;
+};
+
+__device__ __forceinline__ void decode8(const RawCodes& r, F2 (&x)[4])
+{
+    const float step = step_of(r.e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t w = j < 2 ? r.w.x : r.w.y;
+        // 2^23 + code, less 2^23 + 128, times the step: all exact
+        const F2 m = {__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + (2 * j & 3))),
+                      __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + (2 * j + 1 & 3)))};
+        x[j] = mul2(add2(m, {-8388736.0f, -8388736.0f}), {step, step});
+    }
+}
+
+// 8-bit form of 64 successive positions: 8 lanes of 8 (all the row's lanes
+// where it has fewer).  Returns the group's exponent byte.
+template <int S>
+__device__ __forceinline__ uint32_t encode8(const F2 (&x)[4], uint2& codes)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = __float_as_uint(x[j].x) & kAbsMask, b = __float_as_uint(x[j].y) & kAbsMask;
+        top = max(top, max(a, b));
+    }
+#pragma unroll
+    for (int o = 1; o < (S < 8 ? S : 8); o <<= 1)
+        top = max(top, __shfl_xor_sync(kFull, top, o));
+    const uint32_t e = group_exp(top);
+    const float inv = inv_step_of(e);
+    uint32_t q[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        F2 v = x[j];
+        if (e >= kExpTop)
+            v = {group_fix(v.x, e), group_fix(v.y, e)};
+        // as quant_code: the product is exact, so one rounding
+        const F2 r = fma2(v, {inv, inv}, {12583040.0f, 12583040.0f});
+        q[2 * j] = __float_as_uint(r.x);
+        q[2 * j + 1] = __float_as_uint(r.y);
+    }
+    codes.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+    codes.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+    return e;
+}
+
+// What a lane reads of one tile besides dy.
+template <typename T, bool CODES>
+struct Inputs {
+    std::conditional_t<CODES, RawCodes, Raw<T>> v, g;
+};
+
 template <typename T>
-__device__ __forceinline__ void unpack8(const Raw<T>& r, int cnt, float (&x)[8])
-{
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if constexpr (sizeof(T) == 4)
-            x[j] = __uint_as_float(r.w[j]);
-        else
-            x[j] = __uint_as_float(j & 1 ? r.w[j / 2] & 0xffff0000u : r.w[j / 2] << 16);
-    }
-    if (cnt < 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j >= cnt)
-                x[j] = 0.0f;
-    }
-}
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* p, int cnt, const float (&x)[8])
-{
-    if (cnt <= 0)
-        return;
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (VEC) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < cnt)
-                    p[j] = x[j];
-        }
-    } else {
-        // even and odd elements paired from both alignments
-        if (VEC || (cnt == 8 && (reinterpret_cast<uintptr_t>(p) & 2) == 0)) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 q = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-                w[k] = reinterpret_cast<const uint32_t&>(q);
-            }
-            if constexpr (VEC) {
-                *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    reinterpret_cast<uint32_t*>(p)[k] = w[k];
-            }
-        } else if (cnt == 8) {
-            put(p, x[0]);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<__nv_bfloat162*>(p + 1 + 2 * k) =
-                    __floats2bfloat162_rn(x[2 * k + 1], x[2 * k + 2]);
-            put(p + 7, x[7]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < cnt)
-                    put(p + j, x[j]);
-        }
-    }
-}
-
-// Gates and inputs of a lane's 8 positions; the steps past cnt are the
-// identity (f = 1, i = 0).
+__device__ __forceinline__ void values8(const Raw<T>& r, F2 (&x)[4]) { unpack8(r, x); }
 template <typename T>
-__device__ __forceinline__ void gates8(const float (&g)[8], int cnt, float (&f)[8], float (&i)[8])
+__device__ __forceinline__ void values8(const RawCodes& r, F2 (&x)[4]) { decode8(r, x); }
+template <typename T>
+__device__ __forceinline__ void gate_values8(const Raw<T>& r, F2 (&x)[4]) { unpack_gates8(r, x); }
+template <typename T>
+__device__ __forceinline__ void gate_values8(const RawCodes& r, F2 (&x)[4])
 {
+    decode8(r, x);
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        gate<T>(g[j], f[j], i[j]);
-    if (cnt < 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j >= cnt) {
-                f[j] = 1.0f;
-                i[j] = 0.0f;
-            }
+        for (int j = 0; j < 4; ++j)
+            x[j] = {max_nan(x[j].x, kGateMin), max_nan(x[j].y, kGateMin)};
     }
 }
 
+// ------------------------------------------------------------- maps of a tile
 // Inclusive scan of the maps of S lanes (forward: lane order; REV: from the
-// last lane down), and the map of everything before the lane.
+// last lane down).
 template <int S, bool REV>
-__device__ __forceinline__ void lane_scan(float& A, float& H, float& Aex, float& Hex, int sub)
+__device__ __forceinline__ void lane_scan(float& A, float& H, int sub)
 {
     const int pos = REV ? S - 1 - sub : sub;
 #pragma unroll
@@ -230,300 +299,980 @@ __device__ __forceinline__ void lane_scan(float& A, float& H, float& Aex, float&
             A *= a;
         }
     }
-    Aex = 1.0f;
-    Hex = 0.0f;
-    if constexpr (S > 1) {
-        const float a = REV ? __shfl_down_sync(kFull, A, 1, S) : __shfl_up_sync(kFull, A, 1, S);
-        const float h = REV ? __shfl_down_sync(kFull, H, 1, S) : __shfl_up_sync(kFull, H, 1, S);
-        if (pos > 0) {
-            Aex = a;
-            Hex = h;
-        }
-    }
 }
 
-// 8-bit form of 64 successive positions: 8 lanes of 8 (all the row's lanes
-// where it has fewer).
-template <int S, bool VEC>
-__device__ __forceinline__ void encode8(const float (&x)[8], int cnt, int sub, uint8_t* codes,
-                                        uint8_t* exp)
+// The state before a lane's positions (REV: behind them) from the inclusive
+// maps and the state s before all of the lanes; `end` becomes the one after
+// the lane.
+template <int S, bool REV>
+__device__ __forceinline__ float lane_start(float A, float H, float s, int sub, float& end)
 {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(x[j]) & kAbsMask;
-        top = b > top ? b : top;
-    }
-#pragma unroll
-    for (int o = 1; o < (S < 8 ? S : 8); o <<= 1) {
-        const uint32_t b = __shfl_xor_sync(kFull, top, o);
-        top = b > top ? b : top;
-    }
-    const uint32_t e = group_exp(top);
-    const float inv = inv_step_of(e);
-    uint32_t q[8];
-    if (e >= kExpTop) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            q[j] = quant_code(group_fix(x[j], e), inv);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            q[j] = quant_code(x[j], inv);
-    }
-    if (cnt > 0 && (sub & 7) == 0)
-        *exp = (uint8_t)e;
-    if constexpr (VEC) {
-        if (cnt > 0) {
-            uint2 w;
-            w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-            w.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-            *reinterpret_cast<uint2*>(codes) = w;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < cnt)
-                codes[j] = (uint8_t)q[j];
-    }
+    end = fmaf(A, s, H);
+    if constexpr (S == 1)
+        return s;
+    const float prev = REV ? __shfl_down_sync(kFull, end, 1, S) : __shfl_up_sync(kFull, end, 1, S);
+    return sub == (REV ? S - 1 : 0) ? s : prev;
 }
 
-// Eight codes and their group's exponent byte as they sit in memory.
-struct RawCodes {
-    uint32_t w[2];
-    uint32_t e;
+// The forward steps of a lane's positions: f, i = 1 - f, u = i v, and their
+// composed map.  cnt < 8: the steps from cnt on are the identity.
+template <typename T, bool CODES>
+struct Steps {
+    F2 v[4], f[4], i[4], u[4];
+    float A, H;
+    __device__ __forceinline__ void make(const Inputs<T, CODES>& in, int cnt)
+    {
+        F2 g[4];
+        values8<T>(in.v, v);
+        gate_values8<T>(in.g, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            gate2<T>(g[j], f[j], i[j]);
+            u[j] = mul2(i[j], v[j]);
+        }
+        if (cnt < 8) {
+            cut8(f, cnt, 1.0f);
+            cut8(i, cnt, 0.0f);
+            cut8(u, cnt, 0.0f);
+        }
+        A = f[0].x * f[0].y;
+        H = fmaf(f[0].y, u[0].x, u[0].y);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) {
+            H = fmaf(f[j].y, fmaf(f[j].x, H, u[j].x), u[j].y);
+            A = A * f[j].x * f[j].y;
+        }
+    }
+    __device__ __forceinline__ void replay(float s, F2 (&y)[4]) const
+    {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[j].x = fmaf(f[j].x, s, u[j].x);
+            s = y[j].y = fmaf(f[j].y, y[j].x, u[j].y);
+        }
+    }
 };
 
-template <bool VEC>
-__device__ __forceinline__ RawCodes load_codes(const uint8_t* codes, const uint8_t* exp, int cnt)
-{
-    RawCodes r = {{0u, 0u}, 0u};
-    if (cnt > 0) {
-        r.e = __ldg(exp);
-        if constexpr (VEC) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(codes));
-            r.w[0] = q.x;
-            r.w[1] = q.y;
-        } else {
+// The reversed steps c = f (dy + c') of a lane's positions.
+template <typename T, bool CODES>
+struct BackSteps : Steps<T, CODES> {
+    F2 d[4], fd[4];
+    float D;
+    __device__ __forceinline__ void make(const Inputs<T, CODES>& in, const Raw<T>& dy, int cnt)
+    {
+        Steps<T, CODES>::make(in, cnt);
+        unpack8(dy, d);
+        if (cnt < 8)
+            cut8(d, cnt, 0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < cnt)
-                    r.w[j / 4] |= (uint32_t)__ldg(codes + j) << (8 * (j & 3));
+        for (int j = 0; j < 4; ++j)
+            fd[j] = mul2(this->f[j], d[j]);
+        D = fmaf(this->f[3].x, fd[3].y, fd[3].x);
+#pragma unroll
+        for (int j = 2; j >= 0; --j)
+            D = fmaf(this->f[j].x, fmaf(this->f[j].y, D, fd[j].y), fd[j].x);
+    }
+    // dv and dg from the state s before the lane and the c behind it
+    __device__ __forceinline__ void grads(float s, float c, int cnt, F2 (&ov)[4], F2 (&og)[4]) const
+    {
+        const auto &f = this->f, &i = this->i, &u = this->u, &v = this->v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float s1 = fmaf(f[j].x, s, u[j].x);
+            const F2 gap = add2({s, s1}, {-v[j].x, -v[j].y});
+            og[j] = mul2(gap, f[j]);
+            s = fmaf(f[j].y, s1, u[j].y);
         }
+#pragma unroll
+        for (int j = 3; j >= 0; --j) {
+            const float c1 = fmaf(f[j].y, c, fd[j].y);
+            const F2 dh = add2(d[j], {c1, c});
+            ov[j] = mul2(dh, i[j]);
+            og[j] = mul2(og[j], ov[j]);
+            c = fmaf(f[j].x, c1, fd[j].x);
+        }
+        if (cnt < 8) {
+            // i is 0 past the sequence's end, but NaN of a state times 0 is not
+            cut8(ov, cnt, 0.0f);
+            cut8(og, cnt, 0.0f);
+        }
+    }
+};
+
+// ------------------------------------------------------------- data movement
+// VEC rows (bf16, a multiple of 8 elements): a lane's elements are one 16-byte
+// vector.  Other rows are moved as the 16-byte blocks of memory that hold the
+// tile's elements, through an image of them in shared memory, from which lanes
+// take their elements at whatever offset they have; blocks that reach over the
+// tile's ends are written element by element.  (fp32 rows go that way even
+// where they are aligned: a lane's 32 bytes would be two 16-byte accesses 32
+// bytes apart, each half of every sector; B32 C256 L1568 forward 40 us against
+// 34 us through the image.)
+
+__device__ __forceinline__ uint4 lds4(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// Copies the blocks that hold [at, at + bytes) into `dst`, cut at the
+// tensor's ends: base, its first byte, and end, the one behind its last.
+__device__ __forceinline__ void image_copy(uint8_t* dst, const uint8_t* at, int bytes,
+                                           const uint8_t* base, const uint8_t* end, int lane)
+{
+    if (bytes <= 0)
+        return;
+    const uint8_t* a0 = at - (reinterpret_cast<uintptr_t>(at) & 15);
+    const int blocks = (int)((at - a0) + bytes + 15) >> 4;
+    for (int k = lane; k < blocks; k += 32) {
+        const uint8_t* src = a0 + 16 * k;
+        const uint32_t to = smem_u32(dst + 16 * k);
+        if (src >= base) {
+            const long long left = end - src;
+            cp_async_16z(to, src, left < 16 ? (uint32_t)left : 16u);
+        } else {
+            // fp32 tensors may start between 16-byte boundaries
+#pragma unroll
+            for (int q = 0; q < 16; q += 4)
+                if (src + q >= base && src + q < end)
+                    cp_async_4(to + q, src + q);
+        }
+    }
+}
+
+// N words from byte `off` of an image, off % 4 == 0 or (two-byte elements)
+// 2, the same for all lanes but for multiples of 16.
+template <int N, bool HALVES>
+__device__ __forceinline__ void shifted(const uint8_t* img, int off, uint32_t (&r)[N])
+{
+    uint32_t u[N + 4];
+    const uint8_t* p = img + (off & ~15);
+#pragma unroll
+    for (int k = 0; k < N + 4; k += 4) {
+        const uint4 q = lds4(p + 4 * k);
+        u[k] = q.x; u[k + 1] = q.y; u[k + 2] = q.z; u[k + 3] = q.w;
+    }
+    if (off & 8) {
+#pragma unroll
+        for (int k = 0; k < N + 2; ++k)
+            u[k] = u[k + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+        for (int k = 0; k < N + 1; ++k)
+            u[k] = u[k + 1];
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        r[k] = HALVES && (off & 2) ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
+}
+
+// Eight elements at byte `off` of an image.
+template <typename T, bool ONE_ROW>
+__device__ __forceinline__ Raw<T> image_read(const uint8_t* img, int off)
+{
+    Raw<T> r;
+    if constexpr (ONE_ROW) {
+        shifted<Raw<T>::N, sizeof(T) == 2>(img, off, r.w);
+    } else {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(img + (off & ~3));
+        uint32_t u[Raw<T>::N + 1];
+#pragma unroll
+        for (int k = 0; k < Raw<T>::N + 1; ++k)
+            u[k] = p[k];
+#pragma unroll
+        for (int k = 0; k < Raw<T>::N; ++k)
+            r.w[k] = sizeof(T) == 2 && (off & 2) ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
     }
     return r;
 }
 
-__device__ __forceinline__ void decode8(const RawCodes& r, int cnt, float (&x)[8])
+// The 8 codes at byte `off` of an image.
+__device__ __forceinline__ uint2 image_codes(const uint8_t* img, int off)
 {
-    const float step = step_of(r.e);
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(img + (off & ~3));
+    const int sh = 8 * (off & 3);
+    const uint32_t a = p[0], b = p[1], c = p[2];
+    return make_uint2(__funnelshift_r(a, b, sh), __funnelshift_r(b, c, sh));
+}
+
+// Writes the lanes' elements through the warp's image buffer: `count` from p
+// on, this lane's (cnt of them) from element `mine`.
+template <typename T, bool ONE_ROW>
+__device__ __forceinline__ void image_store(T* p, int count, int mine, int cnt, const Raw<T>& r,
+                                            uint8_t* stage, int lane)
+{
+    constexpr int E = 16 / (int)sizeof(T);      // elements a block
+    const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(T);
+    T* img = reinterpret_cast<T*>(stage);
+    __syncwarp();
+    if constexpr (ONE_ROW) {
+        // as they are, from the second block on: blocks are shifted when read
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        x[j] = code_value(__byte_perm(r.w[j / 4], 0u, 0x4440 + (j & 3)), step);
-    if (cnt < 8) {
+        for (int k = 0; k < Raw<T>::N; k += 4)
+            *reinterpret_cast<uint4*>(img + E + mine + k / 4 * E) =
+                make_uint4(r.w[k], r.w[k + 1], r.w[k + 2], r.w[k + 3]);
+        __syncwarp();
+        if (count == kScanTile) {
+            // block k holds elements k E - s on; the first and the one behind
+            // the last are partial unless s = 0
+#pragma unroll
+            for (int k = lane; k < kScanTile / E; k += 32) {
+                if (k == 0 && s != 0)
+                    continue;
+                uint32_t q[4];
+                shifted<4, sizeof(T) == 2>(stage, (E + k * E - s) * (int)sizeof(T), q);
+                *reinterpret_cast<uint4*>(p + k * E - s) = make_uint4(q[0], q[1], q[2], q[3]);
+            }
+            if (s != 0) {
+                const bool low = lane < E - s;
+                const int e = low ? lane : kScanTile - 32 + lane;
+                if (low || lane >= 32 - s)
+                    p[e] = img[E + e];
+            }
+        } else {
+            for (int e = lane; e < count; e += 32)
+                p[e] = img[E + e];
+        }
+    } else {
+        // in the place that memory has for them
+        const T* x = reinterpret_cast<const T*>(r.w);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j >= cnt)
-                x[j] = 0.0f;
+            if (j < cnt)
+                img[s + mine + j] = x[j];
+        __syncwarp();
+        const int blocks = (s + count + E - 1) / E;
+        for (int k = lane; k < blocks; k += 32) {
+            const int e0 = k * E - s;
+            if (e0 >= 0 && e0 + E <= count) {
+                *reinterpret_cast<uint4*>(p + e0) = lds4(stage + 16 * k);
+            } else {
+                for (int j = 0; j < E; ++j)
+                    if (e0 + j >= 0 && e0 + j < count)
+                        p[e0 + j] = img[s + e0 + j];
+            }
+        }
     }
 }
 
-// What a lane reads of one tile, loaded a tile ahead of its use.
-template <typename T, bool CODES>
-struct Inputs {
-    std::conditional_t<CODES, RawCodes, Raw<T>> v, g;
-};
-
-// The row that S lanes of a warp work on, and its tiles of S * 8 positions.
-struct Row {
-    long long row, at;      // row index; its first element
-    long long ntile, ngrp;  // entries of the states array and exponent bytes a row
-    int n;                  // positions of the sequence
-    int L;                  // positions of the row (0: no such row)
-};
-
-__device__ __forceinline__ Row make_row(const ScanArgs& P, long long row)
+// The same for codes: aligned words of memory, single bytes at the ends.
+template <bool ONE_ROW>
+__device__ __forceinline__ void image_store_codes(uint8_t* p, int count, int mine, int cnt, uint2 codes,
+                                                  uint8_t* stage, int lane)
 {
-    Row R;
-    R.row = row;
-    R.at = row * P.L;
-    R.ntile = (P.L + kScanTile - 1ll) / kScanTile;
-    R.ngrp = (P.L + WBMM_SEQ_GROUP - 1ll) / WBMM_SEQ_GROUP;
-    const bool real = row < P.rows;
-    R.L = real ? P.L : 0;
-    R.n = real ? row_len(P.lengths, row, P.C, P.L) : 0;
-    return R;
-}
-
-template <typename T, bool VEC, bool CODES>
-__device__ __forceinline__ Inputs<T, CODES> load_inputs(const ScanArgs& P, const Row& R, long long t0)
-{
-    Inputs<T, CODES> in;
-    const int cnt = clamp8(R.n - t0);
-    if constexpr (CODES) {
-        const long long gi = R.row * R.ngrp + t0 / WBMM_SEQ_GROUP;
-        in.v = load_codes<VEC>(P.v_codes + R.at + t0, P.v_exps + gi, cnt);
-        in.g = load_codes<VEC>(P.g_codes + R.at + t0, P.g_exps + gi, cnt);
+    const int s = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    __syncwarp();
+    if constexpr (ONE_ROW) {
+        *reinterpret_cast<uint2*>(stage + 8 + mine) = codes;
     } else {
-        in.v = load_raw<VEC>(static_cast<const T*>(P.v) + R.at + t0, cnt);
-        in.g = load_raw<VEC>(static_cast<const T*>(P.g) + R.at + t0, cnt);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < cnt)
+                stage[8 + mine + j] = (uint8_t)((j < 4 ? codes.x : codes.y) >> (8 * (j & 3)));
     }
-    return in;
+    __syncwarp();
+    const int words = (s + count + 3) / 4;
+    for (int k = lane; k < words; k += 32) {
+        const int e0 = 4 * k - s;
+        if (e0 >= 0 && e0 + 4 <= count) {
+            const int off = 8 + e0;
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + (off & ~3));
+            *reinterpret_cast<uint32_t*>(p + e0) = __funnelshift_r(w[0], w[1], 8 * (off & 3));
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (e0 + j >= 0 && e0 + j < count)
+                    p[e0 + j] = stage[8 + e0 + j];
+        }
+    }
 }
 
+// Bytes of an image of 256 elements, with room for the reads past its end.
 template <typename T>
-__device__ __forceinline__ void values8(const Raw<T>& r, int cnt, float (&x)[8]) { unpack8(r, cnt, x); }
-template <typename T>
-__device__ __forceinline__ void values8(const RawCodes& r, int cnt, float (&x)[8]) { decode8(r, cnt, x); }
+constexpr int kImage = 256 * (int)sizeof(T) + 48;
 
-// The forward steps of a tile: gates, inputs (1 - f) v, and the composed map.
-template <typename T, bool CODES>
-struct Steps {
-    float v[8], f[8], i[8];
-    float A, H;
-    __device__ __forceinline__ void make(const Inputs<T, CODES>& in, int cnt)
+// ---------------------------------------------------------- rows of many tiles
+// A warp, or a team of warps, walks a row's tiles with the inputs of its next
+// tiles in flight as asynchronous copies into a ring of stages of its own.
+constexpr int kWarps = 4;
+
+// One stage: v and g (maps or codes), dy.
+template <typename T, bool VEC, bool CODES, bool BACK>
+struct Stage {
+    static constexpr int MAP = VEC ? 256 * (int)sizeof(T) : kImage<T>;
+    static constexpr int ARR = !CODES ? MAP : VEC ? 256 : 304;
+    static constexpr int DY = 2 * ARR;
+    static constexpr int BYTES = DY + (BACK ? MAP : 0);
+    // four stages, three of the larger fp32 ones
+    static constexpr int DEPTH = BYTES > 2048 ? 3 : 4;
+    static constexpr int OUT = VEC ? 0 : kImage<T>;     // image of an output
+    static constexpr int WARP = DEPTH * BYTES + OUT;
+};
+
+// One input array of a row as the warp walks it.
+template <int SZ, bool VEC>
+struct Stream {
+    const uint8_t* next;    // of the tile to fetch next: this lane's part (VEC), its first element
+    __device__ __forceinline__ void start(const void* p, long long first, int lane)
     {
-        float g[8];
-        values8<T>(in.v, cnt, v);
-        values8<T>(in.g, cnt, g);
-        gates8<T>(g, cnt, f, i);
-        A = 1.0f;
-        H = 0.0f;
+        next = static_cast<const uint8_t*>(p) + first * SZ + (VEC ? lane * 8 * SZ : 0);
+    }
+    // positions from the tile's start to the end of the sequence
+    __device__ __forceinline__ void fetch(uint8_t* dst, int left, bool inner, const void* base,
+                                          long long elems, int lane) const
+    {
+        if constexpr (VEC) {
+            if (left > lane * 8) {
+                if constexpr (SZ == 1) {
+                    cp_async_8(smem_u32(dst + 8 * lane), next);
+                } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            H = fmaf(f[j], H, i[j] * v[j]);
-            A *= f[j];
+                    for (int k = 0; k < SZ / 2; ++k)
+                        cp_async_16z(smem_u32(dst + 512 * k + 16 * lane), next + 16 * k, 16u);
+                }
+            }
+        } else if (inner && next - 12 >= base) {
+            // a whole tile with a block's worth of the row behind it (and of
+            // the tensor before it: fp32 ones may start anywhere): 16, 32 or
+            // 64 blocks, and one more for the shift
+            const int s = (int)(reinterpret_cast<uintptr_t>(next) & 15);
+            const uint8_t* src = next - s + 16 * lane;
+            if (lane < 16 * SZ)
+                cp_async_16z(smem_u32(dst + 16 * lane), src, 16u);
+            if constexpr (SZ == 4)
+                cp_async_16z(smem_u32(dst + 512 + 16 * lane), src + 512, 16u);
+            if (s != 0 && lane == 0)
+                cp_async_16z(smem_u32(dst + 256 * SZ), src + 256 * SZ, 16u);
+        } else {
+            const uint8_t* b = static_cast<const uint8_t*>(base);
+            image_copy(dst, next, (left < kScanTile ? left : kScanTile) * SZ, b, b + elems * SZ, lane);
         }
+    }
+    __device__ __forceinline__ void advance(int tiles) { next += (long long)tiles * (kScanTile * SZ); }
+};
+
+// Where several warps take one row: a team of the 4 warps of a CTA, or of all
+// CTAs of a cluster.  In each round warp k of the team has the round's k-th
+// tile, publishes the tile's composed map in the shared memory of every CTA of
+// the team, and, after one barrier, applies the maps of the warps before its
+// own to the state that all of them carry from round to round.  Rounds
+// alternate between two slot arrays, so one barrier a round is enough: a warp
+// overwrites a slot only after the next barrier, which its readers have passed
+// by then.  A CTA's last remote access comes before the last barrier, so none
+// reaches a CTA that has ended.
+constexpr int kTeamMax = 8 * kWarps;
+
+struct Team {
+    int ctas, size, me;     // CTAs of the cluster, warps of the team, this warp
+    float2 (*slot)[kTeamMax];
+
+    __device__ __forceinline__ void init(float2 (*s)[kTeamMax])
+    {
+        ctas = (int)cluster_nctarank();
+        size = ctas * kWarps;
+        me = (int)cluster_ctarank() * kWarps + (int)(threadIdx.x >> 5);
+        slot = s;
+        if (ctas > 1)
+            cluster_sync();     // every CTA of the cluster has started
+    }
+    // A and H are the tile's, on every lane.
+    __device__ __forceinline__ void publish(int buf, float A, float H, int lane)
+    {
+        if (ctas == 1) {
+            if (lane == 0)
+                slot[buf][me] = make_float2(A, H);
+            __syncthreads();
+        } else {
+            if (lane < ctas)
+                st_cluster_f2(smem_u32(&slot[buf][me]), (uint32_t)lane, A, H);
+            __syncwarp();
+            cluster_sync();
+        }
+    }
+    // The state before this warp's tile, from the one before the round's
+    // first (REV: behind its last); `s` becomes the one after the round.
+    template <bool REV>
+    __device__ __forceinline__ float join(int buf, float& s) const
+    {
+        float mine = s;
+        for (int k = 0; k < size; k += 4) {
+            float2 m[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                m[q] = slot[buf][REV ? size - 1 - k - q : k + q];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if ((REV ? size - 1 - k - q : k + q) == me)
+                    mine = s;
+                s = fmaf(m[q].x, s, m[q].y);
+            }
+        }
+        return mine;
     }
 };
 
-// Forward, S lanes a row: 32 lanes walk a row's tiles one after the other,
-// fewer lanes take rows of at most 8 * S positions in one tile.
-template <typename T, int S, bool VEC, bool KEEP>
-__global__ void __launch_bounds__(128) scan_fwd_kernel(const ScanArgs P)
+// The four exponent bytes of tile t (0 past the row's last).
+__device__ __forceinline__ uint32_t tile_exps(const uint8_t* row, int t, int ngrp)
 {
-    grid_dep_wait();
-    grid_dep_launch();
-    const int sub = threadIdx.x & (S - 1);
-    const Row R = make_row(P, (long long)blockIdx.x * (128 / S) + threadIdx.x / S);
-    float h = P.h0 && R.L ? P.h0[R.row] : 0.0f;
-    const long long tiles = S == 32 ? R.ntile : 1;
-    Inputs<T, false> nxt = load_inputs<T, VEC, false>(P, R, sub * 8);
-    for (long long t = 0; t < tiles; ++t) {
-        const long long t0 = t * kScanTile + sub * 8;
-        const int cnt = clamp8(R.n - t0), all = clamp8(R.L - t0);
-        const Inputs<T, false> in = nxt;
-        if (S == 32 && t + 1 < tiles)
-            nxt = load_inputs<T, VEC, false>(P, R, t0 + kScanTile);
-        Steps<T, false> st;
-        st.make(in, cnt);
-        float A = st.A, H = st.H, Aex, Hex;
-        lane_scan<S, false>(A, H, Aex, Hex, sub);
-        if (P.states && sub == 0 && t * kScanTile < R.n)
-            P.states[R.row * R.ntile + t] = h;
-        float s = fmaf(Aex, h, Hex), out[8];
+    uint32_t w = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s = fmaf(st.f[j], s, st.i[j] * st.v[j]);
-            out[j] = j < cnt ? s : 0.0f;
-        }
-        store8<VEC>(static_cast<T*>(P.y) + R.at + t0, all, out);
-        if constexpr (KEEP) {
-            const long long gi = R.row * R.ngrp + t0 / WBMM_SEQ_GROUP;
-            float xg[8];
-            values8<T>(in.g, cnt, xg);
-            encode8<S, VEC>(st.v, all, sub, P.v_codes + R.at + t0, P.v_exps + gi);
-            encode8<S, VEC>(xg, all, sub, P.g_codes + R.at + t0, P.g_exps + gi);
-        }
-        h = __shfl_sync(kFull, s, S - 1, S);
-    }
-    if (P.hT && sub == 0 && R.L)
-        P.hT[R.row] = h;
+    for (int b = 0; b < 4; ++b)
+        if (t >= 0 && 4ll * t + b < ngrp)
+            w |= (uint32_t)__ldg(row + 4ll * t + b) << (8 * b);
+    return w;
 }
 
-// Backward, S lanes a row, tiles from the last to the first.
-template <typename T, int S, bool VEC, bool CODES>
-__global__ void __launch_bounds__(128) scan_bwd_kernel(const ScanArgs P)
+// A row and the warp's walk along it.
+struct RowWalk {
+    long long row;
+    int n;              // positions of the sequence
+    int ntile, ngrp;    // of the row
+    int step, from;     // every step-th tile from the from-th on
+    int rounds;
+};
+
+template <bool TEAM>
+__device__ __forceinline__ RowWalk row_walk(const ScanArgs& P, const Team& M)
 {
+    RowWalk w;
+    w.row = TEAM ? (long long)(blockIdx.x / M.ctas)
+                 : (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    w.n = w.row < P.rows ? row_len(P.lengths, w.row, P.C, P.L) : 0;
+    w.ntile = (int)((P.L + kScanTile - 1ll) / kScanTile);
+    w.ngrp = (int)((P.L + WBMM_SEQ_GROUP - 1ll) / WBMM_SEQ_GROUP);
+    w.step = TEAM ? M.size : 1;
+    w.from = TEAM ? M.me : 0;
+    w.rounds = (w.ntile + w.step - 1) / w.step;
+    return w;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> stage_map(const uint8_t* st, int off, int lane)
+{
+    Raw<T> r;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < Raw<T>::N; k += 4) {
+            const uint4 q = lds4(st + 128 * k + 16 * lane);
+            r.w[k] = q.x; r.w[k + 1] = q.y; r.w[k + 2] = q.z; r.w[k + 3] = q.w;
+        }
+    } else {
+        r = image_read<T, true>(st, off + lane * 8 * (int)sizeof(T));
+    }
+    return r;
+}
+
+// Offset of a row's elements from 16-byte boundaries, the same for all of its
+// tiles.
+template <int SZ, bool VEC>
+__device__ __forceinline__ int shift_of(const void* p, long long first)
+{
+    return VEC ? 0 : (int)((reinterpret_cast<uintptr_t>(p) + (unsigned long long)first * SZ) & 15);
+}
+
+// One element type's output of a tile: `count` positions of the row, cnt of
+// them this lane's.
+template <typename T, bool VEC>
+__device__ __forceinline__ void tile_store(T* p, int count, const F2 (&x)[4], uint8_t* out, int lane)
+{
+    const Raw<T> r = pack8<T>(x);
+    if constexpr (VEC) {
+        if (count > lane * 8) {
+#pragma unroll
+            for (int k = 0; k < Raw<T>::N; k += 4)
+                reinterpret_cast<uint4*>(p + lane * 8)[k / 4] =
+                    make_uint4(r.w[k], r.w[k + 1], r.w[k + 2], r.w[k + 3]);
+        }
+    } else if (count > 0) {
+        image_store<T, true>(p, count < kScanTile ? count : kScanTile, lane * 8, 8, r, out, lane);
+    }
+}
+
+__device__ __forceinline__ int lane_count(int left, int lane)
+{
+    const int c = left - lane * 8;
+    return c < 0 ? 0 : c > 8 ? 8 : c;
+}
+
+// Forward: one row a warp, or (TEAM) a CTA or cluster.  KEEP: the 8-bit forms
+// of v and g are written too.
+template <typename T, bool VEC, bool KEEP, bool TEAM>
+__global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const ScanArgs P)
+{
+    using G = Stage<T, VEC, false, false>;
+    constexpr int SZ = (int)sizeof(T);
+    __shared__ __align__(16) uint8_t ring[kWarps][G::WARP];
+    __shared__ float2 slots[2][TEAM ? kTeamMax : 1];
     grid_dep_wait();
     grid_dep_launch();
-    const int sub = threadIdx.x & (S - 1);
-    const Row R = make_row(P, (long long)blockIdx.x * (128 / S) + threadIdx.x / S);
-    const T* dy = static_cast<const T*>(P.dy) + R.at;
-    float c = P.h0 && R.L ? P.h0[R.row] : 0.0f;
-    const long long tiles = S == 32 ? R.ntile : 1;
-    auto state_at = [&](long long t) {
-        return t * kScanTile < R.n ? __ldg(P.states + R.row * R.ntile + t) : 0.0f;
+    const int lane = threadIdx.x & 31;
+    uint8_t* const mine = ring[threadIdx.x >> 5];
+    uint8_t* const out = mine + G::DEPTH * G::BYTES;
+    Team M = {};
+    if constexpr (TEAM)
+        M.init(reinterpret_cast<float2(*)[kTeamMax]>(slots));
+    const RowWalk w = row_walk<TEAM>(P, M);
+    if (w.row >= P.rows)
+        return;         // no teams: they have a row each
+    const long long base = w.row * P.L, elems = P.rows * P.L;
+    long long at = base + (long long)w.from * kScanTile;    // the tile's first element
+    const int off_v = shift_of<SZ, VEC>(P.v, at), off_g = shift_of<SZ, VEC>(P.g, at);
+    Stream<SZ, VEC> fv, fg;
+    fv.start(P.v, at, lane);
+    fg.start(P.g, at, lane);
+    const int hop = w.step * kScanTile;
+    int left = w.n - w.from * kScanTile;            // from the tile's start to the sequence's end
+    int far = left, stored = P.L - w.from * kScanTile;
+    uint8_t* into = mine;                           // the stage to fetch into
+    const uint8_t* const last = mine + (G::DEPTH - 1) * G::BYTES;
+    auto prefetch = [&] {
+        if (far > 0) {
+            fv.fetch(into, far, far >= kScanTile + 16, P.v, elems, lane);
+            fg.fetch(into + G::ARR, far, far >= kScanTile + 16, P.g, elems, lane);
+        }
+        fv.advance(w.step);
+        fg.advance(w.step);
+        far -= hop;
+        into = into == last ? mine : into + G::BYTES;
+        cp_async_commit();
     };
-    long long t0 = (tiles - 1) * kScanTile + sub * 8;
-    Inputs<T, CODES> nxt = load_inputs<T, VEC, CODES>(P, R, t0);
-    Raw<T> nxt_dy = load_raw<VEC>(dy + t0, clamp8(R.n - t0));
-    float nxt_h = state_at(tiles - 1);
-    for (long long t = tiles - 1; t >= 0; --t, t0 -= kScanTile) {
-        const int cnt = clamp8(R.n - t0), all = clamp8(R.L - t0);
-        const Inputs<T, CODES> in = nxt;
-        const Raw<T> rdy = nxt_dy;
-        const float h = nxt_h;
-        if (S == 32 && t > 0) {
-            nxt = load_inputs<T, VEC, CODES>(P, R, t0 - kScanTile);
-            nxt_dy = load_raw<VEC>(dy + t0 - kScanTile, clamp8(R.n - t0 + kScanTile));
-            nxt_h = state_at(t - 1);
-        }
-        Steps<T, CODES> st;
-        st.make(in, cnt);
-        float d[8];
-        unpack8(rdy, cnt, d);
-        float A = st.A, H = st.H, Ar = st.A, D = 0.0f, Aex, Hex, Dex;
 #pragma unroll
-        for (int j = 7; j >= 0; --j)
-            D = st.f[j] * (d[j] + D);
-        lane_scan<S, false>(A, H, Aex, Hex, sub);
-        float s = fmaf(Aex, h, Hex), before[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            before[j] = s;
-            s = fmaf(st.f[j], s, st.i[j] * st.v[j]);
+    for (int k = 0; k < G::DEPTH - 1; ++k)
+        prefetch();
+    float h = P.h0 ? P.h0[w.row] : 0.0f;
+    float kept = 0.0f;      // lane k: the state before the k-th of 32 rounds' tiles
+    const uint8_t* st = mine;
+    for (int k = 0; k < w.rounds; ++k) {
+        if constexpr (!VEC)
+            __syncwarp();       // every lane has read the stage that is fetched into next
+        prefetch();
+        cp_async_wait_group<G::DEPTH - 1>();
+        if constexpr (!VEC)
+            __syncwarp();
+        const int cnt = left >= kScanTile ? 8 : lane_count(left, lane);
+        Inputs<T, false> in;
+        in.v = stage_map<T, VEC>(st, off_v, lane);
+        in.g = stage_map<T, VEC>(st + G::ARR, off_g, lane);
+        st = st == last ? mine : st + G::BYTES;
+        Steps<T, false> s8;
+        s8.make(in, cnt);
+        float A = s8.A, H = s8.H, hin = h, end;
+        lane_scan<32, false>(A, H, lane);
+        if constexpr (TEAM) {
+            M.publish(k & 1, __shfl_sync(kFull, A, 31), __shfl_sync(kFull, H, 31), lane);
+            hin = M.join<false>(k & 1, h);
         }
-        lane_scan<S, true>(Ar, D, Aex, Dex, sub);
-        float cc = fmaf(Aex, c, Dex), ov[8], og[8];
+        const float s = lane_start<32, false>(A, H, hin, lane, end);
+        if constexpr (!TEAM)
+            h = __shfl_sync(kFull, end, 31);
+        F2 y[4];
+        s8.replay(s, y);
+        if (cnt < 8)
+            cut8(y, cnt, 0.0f);
+        tile_store<T, VEC>(static_cast<T*>(P.y) + at, stored, y, out, lane);
+        if constexpr (KEEP) {
+            if (stored > 0) {
+                const int all = lane_count(stored, lane);
+                const long long grp = w.row * w.ngrp + (long long)(k * w.step + w.from) * 4 + lane / 8;
 #pragma unroll
-        for (int j = 7; j >= 0; --j) {
-            const float dh = d[j] + cc;
-            ov[j] = dh * st.i[j];
-            cc = st.f[j] * dh;
-            og[j] = ov[j] * st.f[j] * (before[j] - st.v[j]);
+                for (int a = 0; a < 2; ++a) {
+                    F2 x[4];
+                    values8<T>(a ? in.g : in.v, x);
+                    if (cnt < 8)
+                        cut8(x, cnt, 0.0f);
+                    uint2 code;
+                    const uint32_t e = encode8<32>(x, code);
+                    uint8_t* p = (a ? P.g_codes : P.v_codes) + at;
+                    if constexpr (VEC) {
+                        if (all > 0)
+                            *reinterpret_cast<uint2*>(p + lane * 8) = code;
+                    } else {
+                        image_store_codes<true>(p, stored < kScanTile ? stored : kScanTile, lane * 8, 8,
+                                                code, out, lane);
+                    }
+                    if (all > 0 && (lane & 7) == 0)
+                        (a ? P.g_exps : P.v_exps)[grp] = (uint8_t)e;
+                }
+            }
         }
-        if (cnt < 8) {
-            // i is 0 past the sequence's end, but NaN of a state times 0 is not
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j >= cnt)
-                    ov[j] = og[j] = 0.0f;
+        if (P.states) {
+            if (lane == (k & 31))
+                kept = hin;
+            if ((k & 31) == 31 || k == w.rounds - 1) {
+                const int t = ((k & ~31) + lane) * w.step + w.from;
+                if (lane <= (k & 31) && (long long)t * kScanTile < w.n)
+                    P.states[w.row * w.ntile + t] = kept;
+            }
         }
-        store8<VEC>(static_cast<T*>(P.dv) + R.at + t0, all, ov);
-        store8<VEC>(static_cast<T*>(P.dg) + R.at + t0, all, og);
-        c = __shfl_sync(kFull, cc, 0, S);
+        left -= hop;
+        stored -= hop;
+        at += hop;
     }
-    if (P.hT && sub == 0 && R.L)
-        P.hT[R.row] = c;
+    if (P.hT && lane == 0 && (!TEAM || M.me == 0))
+        P.hT[w.row] = h;
 }
 
-// One position of every row; one thread a row.
-template <typename T>
+// Backward, tiles from the last to the first.  CODES: v and g from their
+// 8-bit forms.
+template <typename T, bool VEC, bool CODES, bool TEAM>
+__global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
+{
+    using G = Stage<T, VEC, CODES, true>;
+    constexpr int SZ = (int)sizeof(T), IN = CODES ? 1 : SZ;
+    __shared__ __align__(16) uint8_t ring[kWarps][G::WARP];
+    __shared__ float2 slots[2][TEAM ? kTeamMax : 1];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    uint8_t* const mine = ring[threadIdx.x >> 5];
+    uint8_t* const out = mine + G::DEPTH * G::BYTES;
+    Team M = {};
+    if constexpr (TEAM)
+        M.init(reinterpret_cast<float2(*)[kTeamMax]>(slots));
+    const RowWalk w = row_walk<TEAM>(P, M);
+    if (w.row >= P.rows)
+        return;         // no teams: they have a row each
+    const long long base = w.row * P.L, elems = P.rows * P.L;
+    const int t_last = (w.rounds - 1) * w.step + w.from;
+    long long at = base + (long long)t_last * kScanTile;
+    const void* const sv = CODES ? P.v_codes : P.v;
+    const void* const sg = CODES ? P.g_codes : P.g;
+    const int off_v = shift_of<IN, VEC>(sv, at), off_g = shift_of<IN, VEC>(sg, at);
+    const int off_d = shift_of<SZ, VEC>(P.dy, at);
+    Stream<IN, VEC> fv, fg;
+    Stream<SZ, VEC> fd;
+    fv.start(sv, at, lane);
+    fg.start(sg, at, lane);
+    fd.start(P.dy, at, lane);
+    const int hop = w.step * kScanTile;
+    int left = (int)(w.n - (long long)t_last * kScanTile);
+    int far = left, stored = (int)(P.L - (long long)t_last * kScanTile);
+    int togo = w.rounds;                            // tiles to fetch
+    uint8_t* into = mine;
+    const uint8_t* const last = mine + (G::DEPTH - 1) * G::BYTES;
+    auto prefetch = [&] {
+        if (togo > 0 && far > 0) {
+            fv.fetch(into, far, far >= kScanTile + 16, sv, elems, lane);
+            fg.fetch(into + G::ARR, far, far >= kScanTile + 16, sg, elems, lane);
+            fd.fetch(into + G::DY, far, far >= kScanTile + 16, P.dy, elems, lane);
+        }
+        fv.advance(-w.step);
+        fg.advance(-w.step);
+        fd.advance(-w.step);
+        far += togo > 0 ? hop : 0;
+        --togo;
+        into = into == last ? mine : into + G::BYTES;
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < G::DEPTH - 1; ++k)
+        prefetch();
+    float c = P.h0 ? P.h0[w.row] : 0.0f;
+    // lane k: the state before the tile, and the exponent bytes, of the k-th of
+    // 32 rounds
+    float states = 0.0f;
+    uint32_t ve = 0, ge = 0;
+    const uint8_t* st = mine;
+    for (int k = 0; k < w.rounds; ++k) {
+        if ((k & 31) == 0) {
+            const int t = t_last - (k + lane) * w.step;
+            states = t >= 0 && (long long)t * kScanTile < w.n ? __ldg(P.states + w.row * w.ntile + t) : 0.0f;
+            if constexpr (CODES) {
+                ve = tile_exps(P.v_exps + w.row * w.ngrp, t, w.ngrp);
+                ge = tile_exps(P.g_exps + w.row * w.ngrp, t, w.ngrp);
+            }
+        }
+        if constexpr (!VEC)
+            __syncwarp();       // every lane has read the stage that is fetched into next
+        prefetch();
+        cp_async_wait_group<G::DEPTH - 1>();
+        if constexpr (!VEC)
+            __syncwarp();
+        const int cnt = left >= kScanTile ? 8 : lane_count(left, lane);
+        Inputs<T, CODES> in;
+        if constexpr (CODES) {
+            if constexpr (VEC) {
+                in.v.w = *reinterpret_cast<const uint2*>(st + 8 * lane);
+                in.g.w = *reinterpret_cast<const uint2*>(st + G::ARR + 8 * lane);
+            } else {
+                in.v.w = image_codes(st, off_v + 8 * lane);
+                in.g.w = image_codes(st + G::ARR, off_g + 8 * lane);
+            }
+            const uint32_t sel = 0x4440 + lane / 8;
+            in.v.e = __byte_perm(__shfl_sync(kFull, ve, k & 31), 0u, sel);
+            in.g.e = __byte_perm(__shfl_sync(kFull, ge, k & 31), 0u, sel);
+        } else {
+            in.v = stage_map<T, VEC>(st, off_v, lane);
+            in.g = stage_map<T, VEC>(st + G::ARR, off_g, lane);
+        }
+        const Raw<T> dy = stage_map<T, VEC>(st + G::DY, off_d, lane);
+        st = st == last ? mine : st + G::BYTES;
+        const float h = __shfl_sync(kFull, states, k & 31);
+        BackSteps<T, CODES> s8;
+        s8.make(in, dy, cnt);
+        float A = s8.A, D = s8.D, cin = c, end;
+        lane_scan<32, true>(A, D, lane);
+        if constexpr (TEAM) {
+            M.publish(k & 1, __shfl_sync(kFull, A, 0), __shfl_sync(kFull, D, 0), lane);
+            cin = M.join<true>(k & 1, c);
+        }
+        const float cc = lane_start<32, true>(A, D, cin, lane, end);
+        if constexpr (!TEAM)
+            c = __shfl_sync(kFull, end, 0);
+        float A2 = s8.A, H = s8.H;
+        lane_scan<32, false>(A2, H, lane);
+        const float s = lane_start<32, false>(A2, H, h, lane, end);
+        F2 ov[4], og[4];
+        s8.grads(s, cc, cnt, ov, og);
+        tile_store<T, VEC>(static_cast<T*>(P.dv) + at, stored, ov, out, lane);
+        tile_store<T, VEC>(static_cast<T*>(P.dg) + at, stored, og, out, lane);
+        left += hop;
+        stored += hop;
+        at -= hop;
+    }
+    if (P.hT && lane == 0 && (!TEAM || M.me == 0))
+        P.hT[w.row] = c;
+}
+
+// ---------------------------------------------------------------- short rows
+// Rows of at most 8 S positions: S = 1, 4 or 16 lanes a row, 32 / S rows a
+// warp, which are neighbours in memory.
+template <int S>
+struct Group {
+    long long row0, row;    // the warp's first row; this lane's
+    int sub, n, L;          // lane within the row; its positions (sequence, row)
+    int count, mine;        // elements of the warp's rows; this lane's first among them
+    int cnt, all;           // this lane's positions (sequence, row)
+    __device__ __forceinline__ void init(const ScanArgs& P, int lane)
+    {
+        row0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (32 / S);
+        row = row0 + lane / S;
+        sub = lane & (S - 1);
+        const bool real = row < P.rows;
+        L = real ? P.L : 0;
+        n = real ? row_len(P.lengths, row, P.C, P.L) : 0;
+        const long long rows = P.rows - row0;
+        count = (rows < 0 ? 0 : rows > 32 / S ? 32 / S : (int)rows) * P.L;
+        mine = lane / S * P.L + sub * 8;
+        cnt = min(max(n - sub * 8, 0), 8);
+        all = min(max(L - sub * 8, 0), 8);
+    }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void group_fetch(uint8_t* img, const void* base, long long first, int count,
+                                            long long elems, int lane)
+{
+    if constexpr (!VEC) {
+        const uint8_t* b = static_cast<const uint8_t*>(base);
+        image_copy(img, b + first * (long long)sizeof(T), count * (int)sizeof(T), b,
+                   b + elems * (long long)sizeof(T), lane);
+    }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> group_map(const uint8_t* img, const void* base, long long first, int mine,
+                                            int cnt)
+{
+    Raw<T> r = {};
+    const T* p = static_cast<const T*>(base) + first;
+    if constexpr (VEC) {
+        if (cnt > 0) {
+#pragma unroll
+            for (int k = 0; k < Raw<T>::N; k += 4) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + mine) + k / 4);
+                r.w[k] = q.x; r.w[k + 1] = q.y; r.w[k + 2] = q.z; r.w[k + 3] = q.w;
+            }
+        }
+    } else {
+        r = image_read<T, false>(img, (int)(reinterpret_cast<uintptr_t>(p) & 15) + mine * (int)sizeof(T));
+    }
+    return r;
+}
+
+template <bool VEC>
+__device__ __forceinline__ RawCodes group_codes(const uint8_t* img, const uint8_t* base, const uint8_t* exp,
+                                                long long first, int mine, int cnt)
+{
+    RawCodes r = {};
+    if (cnt > 0)
+        r.e = __ldg(exp);
+    const uint8_t* p = base + first;
+    if constexpr (VEC) {
+        if (cnt > 0)
+            r.w = __ldg(reinterpret_cast<const uint2*>(p + mine));
+    } else {
+        r.w = image_codes(img, (int)(reinterpret_cast<uintptr_t>(p) & 15) + mine);
+    }
+    return r;
+}
+
+template <typename T, bool VEC, int S>
+__device__ __forceinline__ void group_store(T* base, const Group<S>& w, long long first, const F2 (&x)[4],
+                                            uint8_t* img, int lane)
+{
+    const Raw<T> r = pack8<T>(x);
+    if constexpr (VEC) {
+        if (w.all > 0) {
+#pragma unroll
+            for (int k = 0; k < Raw<T>::N; k += 4)
+                reinterpret_cast<uint4*>(base + first + w.mine)[k / 4] =
+                    make_uint4(r.w[k], r.w[k + 1], r.w[k + 2], r.w[k + 3]);
+        }
+    } else {
+        image_store<T, false>(base + first, w.count, w.mine, w.all, r, img, lane);
+    }
+}
+
+template <typename T, int S, bool VEC, bool KEEP>
+__global__ void __launch_bounds__(32 * kWarps) scan_fwd_short_kernel(const ScanArgs P)
+{
+    __shared__ __align__(16) uint8_t images[kWarps][VEC ? 16 : 2 * kImage<T>];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    uint8_t* const img = images[threadIdx.x >> 5];
+    Group<S> w;
+    w.init(P, lane);
+    const long long first = w.row0 * P.L, elems = P.rows * P.L;
+    group_fetch<T, VEC>(img, P.v, first, w.count, elems, lane);
+    group_fetch<T, VEC>(img + kImage<T>, P.g, first, w.count, elems, lane);
+    cp_async_wait_all();
+    __syncwarp();
+    Inputs<T, false> in;
+    in.v = group_map<T, VEC>(img, P.v, first, w.mine, w.cnt);
+    in.g = group_map<T, VEC>(img + kImage<T>, P.g, first, w.mine, w.cnt);
+    const float h = P.h0 && w.L > 0 ? P.h0[w.row] : 0.0f;
+    Steps<T, false> s8;
+    s8.make(in, w.cnt);
+    float A = s8.A, H = s8.H, end;
+    lane_scan<S, false>(A, H, w.sub);
+    const float s = lane_start<S, false>(A, H, h, w.sub, end);
+    F2 y[4];
+    s8.replay(s, y);
+    if (w.cnt < 8)
+        cut8(y, w.cnt, 0.0f);
+    group_store<T, VEC>(static_cast<T*>(P.y), w, first, y, img, lane);
+    if constexpr (KEEP) {
+        const int ngrp = (P.L + WBMM_SEQ_GROUP - 1) / WBMM_SEQ_GROUP;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            F2 x[4];
+            values8<T>(a ? in.g : in.v, x);
+            cut8(x, w.cnt, 0.0f);
+            uint2 code;
+            const uint32_t e = encode8<S>(x, code);
+            uint8_t* p = (a ? P.g_codes : P.v_codes) + first;
+            if constexpr (VEC) {
+                if (w.all > 0)
+                    *reinterpret_cast<uint2*>(p + w.mine) = code;
+            } else {
+                image_store_codes<false>(p, w.count, w.mine, w.all, code, img, lane);
+            }
+            if (w.all > 0 && (w.sub & 7) == 0)
+                (a ? P.g_exps : P.v_exps)[w.row * ngrp + w.sub / 8] = (uint8_t)e;
+        }
+    }
+    if (P.states && w.sub == 0 && w.n > 0)
+        P.states[w.row] = h;
+    if (P.hT && w.sub == S - 1 && w.L > 0)
+        P.hT[w.row] = end;
+}
+
+template <typename T, int S, bool VEC, bool CODES>
+__global__ void __launch_bounds__(32 * kWarps) scan_bwd_short_kernel(const ScanArgs P)
+{
+    __shared__ __align__(16) uint8_t images[kWarps][VEC ? 16 : 3 * kImage<T>];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    uint8_t* const img = images[threadIdx.x >> 5];
+    Group<S> w;
+    w.init(P, lane);
+    const long long first = w.row0 * P.L, elems = P.rows * P.L;
+    if constexpr (CODES) {
+        group_fetch<uint8_t, VEC>(img, P.v_codes, first, w.count, elems, lane);
+        group_fetch<uint8_t, VEC>(img + kImage<T>, P.g_codes, first, w.count, elems, lane);
+    } else {
+        group_fetch<T, VEC>(img, P.v, first, w.count, elems, lane);
+        group_fetch<T, VEC>(img + kImage<T>, P.g, first, w.count, elems, lane);
+    }
+    group_fetch<T, VEC>(img + 2 * kImage<T>, P.dy, first, w.count, elems, lane);
+    cp_async_wait_all();
+    __syncwarp();
+    Inputs<T, CODES> in;
+    if constexpr (CODES) {
+        const int ngrp = (P.L + WBMM_SEQ_GROUP - 1) / WBMM_SEQ_GROUP;
+        const long long grp = w.row * ngrp + w.sub / 8;
+        in.v = group_codes<VEC>(img, P.v_codes, P.v_exps + grp, first, w.mine, w.cnt);
+        in.g = group_codes<VEC>(img + kImage<T>, P.g_codes, P.g_exps + grp, first, w.mine, w.cnt);
+    } else {
+        in.v = group_map<T, VEC>(img, P.v, first, w.mine, w.cnt);
+        in.g = group_map<T, VEC>(img + kImage<T>, P.g, first, w.mine, w.cnt);
+    }
+    const Raw<T> dy = group_map<T, VEC>(img + 2 * kImage<T>, P.dy, first, w.mine, w.cnt);
+    const float c = P.h0 && w.L > 0 ? P.h0[w.row] : 0.0f;
+    const float h = w.n > 0 ? __ldg(P.states + w.row) : 0.0f;
+    BackSteps<T, CODES> s8;
+    s8.make(in, dy, w.cnt);
+    float A = s8.A, D = s8.D, end, after;
+    lane_scan<S, true>(A, D, w.sub);
+    const float cc = lane_start<S, true>(A, D, c, w.sub, end);
+    float A2 = s8.A, H = s8.H;
+    lane_scan<S, false>(A2, H, w.sub);
+    const float s = lane_start<S, false>(A2, H, h, w.sub, after);
+    F2 ov[4], og[4];
+    s8.grads(s, cc, w.cnt, ov, og);
+    group_store<T, VEC>(static_cast<T*>(P.dv), w, first, ov, img, lane);
+    group_store<T, VEC>(static_cast<T*>(P.dg), w, first, og, img, lane);
+    if (P.hT && w.sub == 0 && w.L > 0)
+        P.hT[w.row] = end;
+}
+
+// ------------------------------------------------------------- one position
+// One position of every row, V rows a thread: 1, or 8 as 16-byte vectors.
+template <typename T, int V>
 __global__ void __launch_bounds__(128)
     scan_step_kernel(const T* __restrict__ v, const T* __restrict__ g, const float* h, T* y,
                      float* h_next, long long rows)
 {
+    const long long r = ((long long)blockIdx.x * 128 + threadIdx.x) * V;
     grid_dep_wait();
     grid_dep_launch();
-    const long long r = (long long)blockIdx.x * 128 + threadIdx.x;
     if (r >= rows)
         return;
-    float f, i;
-    gate<T>(to_f(g[r]), f, i);
-    const float s = fmaf(f, h[r], i * to_f(v[r]));
-    put(y + r, s);
-    h_next[r] = s;
+    if constexpr (V == 1) {
+        F2 f, i;
+        const float a = sizeof(T) == 2 ? max_nan(to_f(g[r]), kGateMin) : to_f(g[r]);
+        gate2<T>({a, a}, f, i);
+        const float s = fmaf(f.x, h[r], i.x * to_f(v[r]));
+        put(y + r, s);
+        h_next[r] = s;
+    } else {
+        Raw<T> rv, rg;
+        F2 xv[4], xg[4], s[4];
+#pragma unroll
+        for (int k = 0; k < Raw<T>::N; k += 4) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(v + r) + k / 4);
+            const uint4 b = __ldg(reinterpret_cast<const uint4*>(g + r) + k / 4);
+            rv.w[k] = a.x; rv.w[k + 1] = a.y; rv.w[k + 2] = a.z; rv.w[k + 3] = a.w;
+            rg.w[k] = b.x; rg.w[k + 1] = b.y; rg.w[k + 2] = b.z; rg.w[k + 3] = b.w;
+        }
+        const float4 h0 = *reinterpret_cast<const float4*>(h + r);
+        const float4 h1 = *reinterpret_cast<const float4*>(h + r + 4);
+        const F2 was[4] = {{h0.x, h0.y}, {h0.z, h0.w}, {h1.x, h1.y}, {h1.z, h1.w}};
+        unpack8(rv, xv);
+        unpack_gates8(rg, xg);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            F2 f, i;
+            gate2<T>(xg[j], f, i);
+            s[j] = fma2(f, was[j], mul2(i, xv[j]));
+        }
+        const Raw<T> out = pack8<T>(s);
+#pragma unroll
+        for (int k = 0; k < Raw<T>::N; k += 4)
+            reinterpret_cast<uint4*>(y + r)[k / 4] =
+                make_uint4(out.w[k], out.w[k + 1], out.w[k + 2], out.w[k + 3]);
+        *reinterpret_cast<float4*>(h_next + r) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+        *reinterpret_cast<float4*>(h_next + r + 4) = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
+    }
 }
 
 cudaError_t done(cudaError_t e)
@@ -534,57 +1283,88 @@ cudaError_t done(cudaError_t e)
     return cudaGetLastError();
 }
 
-}  // namespace
-
-namespace {
-
 template <typename T, int S, bool VEC, bool AUX>
-cudaError_t row_launch(const ScanArgs& A, bool backward, const Launch& L)
+cudaError_t short_launch(const ScanArgs& A, bool backward, const Launch& L)
 {
-    const dim3 grid((unsigned)((A.rows + 128 / S - 1) / (128 / S))), block(128);
-    return done(backward ? launch_pdl(scan_bwd_kernel<T, S, VEC, AUX>, grid, block, 0, L.stream, A)
-                         : launch_pdl(scan_fwd_kernel<T, S, VEC, AUX>, grid, block, 0, L.stream, A));
+    const long long per = 32 / S * kWarps;
+    const dim3 grid((unsigned)((A.rows + per - 1) / per)), block(32 * kWarps);
+    return done(backward ? launch_pdl(scan_bwd_short_kernel<T, S, VEC, AUX>, grid, block, 0, L.stream, A)
+                         : launch_pdl(scan_fwd_short_kernel<T, S, VEC, AUX>, grid, block, 0, L.stream, A));
 }
 
-// Lanes a row: as few as hold it in one tile of 8 positions a lane (1, 4 or
-// 16), so that short rows leave no lanes idle, or a warp that walks it.
+// A warp a row.
+template <typename T, bool VEC, bool AUX>
+cudaError_t row_launch(const ScanArgs& A, bool backward, const Launch& L)
+{
+    const dim3 grid((unsigned)((A.rows + kWarps - 1) / kWarps)), block(32 * kWarps);
+    return done(backward ? launch_pdl(scan_bwd_kernel<T, VEC, AUX, false>, grid, block, 0, L.stream, A)
+                         : launch_pdl(scan_fwd_kernel<T, VEC, AUX, false>, grid, block, 0, L.stream, A));
+}
+
+// The warps of `ctas` CTAs (a cluster) a row.
+template <typename T, bool VEC, bool AUX>
+cudaError_t team_launch(const ScanArgs& A, bool backward, int ctas, const Launch& L)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(A.rows * ctas));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return done(cudaLaunchKernelEx(&cfg,
+                                   backward ? scan_bwd_kernel<T, VEC, AUX, true>
+                                            : scan_fwd_kernel<T, VEC, AUX, true>,
+                                   A));
+}
+
+// Warps a row: one where that gives an SM 10 of them, else a team of 4, 8, 16
+// or 32 that does, so far as a row has that many tiles.  Measured, forward and
+// backward: 8192 rows of 3136 positions 28 and 43 us with a warp each, 39 and
+// 64 us with teams of 4; 768 rows of 50176 72 and 100 us, 57 and 78 us with
+// teams of 4, 78 and 104 us with teams of 8; 128 rows of 65536 31 and 51 us
+// with teams of 4, 24 and 37 us with 16, 23 and 43 us with 32.
+int team_for(long long rows, int L, int num_sms)
+{
+    const long long tiles = ((long long)L + kScanTile - 1) / kScanTile;
+    int team = 1;
+    while (team < kTeamMax && rows * team < 10ll * num_sms && 2 * team <= tiles)
+        team = team == 1 ? 4 : 2 * team;
+    return team;
+}
+
 template <typename T, bool VEC, bool AUX>
 cudaError_t lanes_launch(const ScanArgs& A, bool backward, const Launch& L)
 {
     if (A.L <= 8)
-        return row_launch<T, 1, VEC, AUX>(A, backward, L);
+        return short_launch<T, 1, VEC, AUX>(A, backward, L);
     if (A.L <= 32)
-        return row_launch<T, 4, VEC, AUX>(A, backward, L);
+        return short_launch<T, 4, VEC, AUX>(A, backward, L);
     if (A.L <= 128)
-        return row_launch<T, 16, VEC, AUX>(A, backward, L);
-    return row_launch<T, 32, VEC, AUX>(A, backward, L);
-}
-
-// Whole 16-byte vectors everywhere: rows of a multiple of 8 elements in
-// buffers that start at 16-byte boundaries (bf16 ones always do).
-bool vector_rows(const ScanArgs& A)
-{
-    uintptr_t all = 0;
-    for (const void* p : {A.v, A.g, (const void*)A.y, A.dy, (const void*)A.dv, (const void*)A.dg})
-        all |= reinterpret_cast<uintptr_t>(p);
-    return A.L % 8 == 0 && all % 16 == 0;
+        return short_launch<T, 16, VEC, AUX>(A, backward, L);
+    const int team = team_for(A.rows, A.L, L.num_sms);
+    if (team > 1)
+        return team_launch<T, VEC, AUX>(A, backward, team / kWarps, L);
+    return row_launch<T, VEC, AUX>(A, backward, L);
 }
 
 cudaError_t scan_launch(const ScanArgs& A, bool is_bf16, bool backward, const Launch& L)
 {
-    const bool vec = vector_rows(A), aux = A.v_codes != nullptr;
-    if (is_bf16) {
-        if (vec)
-            return aux ? lanes_launch<__nv_bfloat16, true, true>(A, backward, L)
-                       : lanes_launch<__nv_bfloat16, true, false>(A, backward, L);
-        return aux ? lanes_launch<__nv_bfloat16, false, true>(A, backward, L)
-                   : lanes_launch<__nv_bfloat16, false, false>(A, backward, L);
-    }
-    if (vec)
-        return aux ? lanes_launch<float, true, true>(A, backward, L)
-                   : lanes_launch<float, true, false>(A, backward, L);
-    return aux ? lanes_launch<float, false, true>(A, backward, L)
-               : lanes_launch<float, false, false>(A, backward, L);
+    const bool aux = A.v_codes != nullptr;
+    if (!is_bf16)
+        return aux ? lanes_launch<float, false, true>(A, backward, L)
+                   : lanes_launch<float, false, false>(A, backward, L);
+    if (A.L % 8 == 0)
+        return aux ? lanes_launch<__nv_bfloat16, true, true>(A, backward, L)
+                   : lanes_launch<__nv_bfloat16, true, false>(A, backward, L);
+    return aux ? lanes_launch<__nv_bfloat16, false, true>(A, backward, L)
+               : lanes_launch<__nv_bfloat16, false, false>(A, backward, L);
 }
 
 }  // namespace
@@ -599,18 +1379,33 @@ cudaError_t scan_backward_launch(const ScanArgs& A, bool is_bf16, const Launch& 
     return scan_launch(A, is_bf16, true, L);
 }
 
+namespace {
+
+template <typename T>
+cudaError_t step_launch(const void* v, const void* g, const float* h, void* y, float* h_next,
+                        long long rows, const Launch& L)
+{
+    // 8 rows a thread once that leaves an SM two blocks of threads, where the
+    // buffers allow it: 256 x 8192 bf16 rows take 17.9 us one a thread
+    uintptr_t all = 0;
+    for (const void* p : {v, g, (const void*)h, (const void*)y, (const void*)h_next})
+        all |= reinterpret_cast<uintptr_t>(p);
+    const bool wide = rows % 8 == 0 && all % 16 == 0 && rows >= 2048ll * L.num_sms;
+    const long long threads = wide ? rows / 8 : rows;
+    const dim3 grid((unsigned)((threads + 127) / 128)), block(128);
+    const T *pv = static_cast<const T*>(v), *pg = static_cast<const T*>(g);
+    T* py = static_cast<T*>(y);
+    return done(wide ? launch_pdl(scan_step_kernel<T, 8>, grid, block, 0, L.stream, pv, pg, h, py, h_next, rows)
+                     : launch_pdl(scan_step_kernel<T, 1>, grid, block, 0, L.stream, pv, pg, h, py, h_next, rows));
+}
+
+}  // namespace
+
 cudaError_t scan_step_launch(const void* v, const void* g, const float* h, void* y, float* h_next,
                              long long rows, bool is_bf16, const Launch& L)
 {
-    const dim3 grid((unsigned)((rows + 127) / 128)), block(128);
-    return done(
-        is_bf16 ? launch_pdl(scan_step_kernel<__nv_bfloat16>, grid, block, 0, L.stream,
-                             static_cast<const __nv_bfloat16*>(v),
-                             static_cast<const __nv_bfloat16*>(g), h,
-                             static_cast<__nv_bfloat16*>(y), h_next, rows)
-                : launch_pdl(scan_step_kernel<float>, grid, block, 0, L.stream,
-                             static_cast<const float*>(v), static_cast<const float*>(g), h,
-                             static_cast<float*>(y), h_next, rows));
+    return is_bf16 ? step_launch<__nv_bfloat16>(v, g, h, y, h_next, rows, L)
+                   : step_launch<float>(v, g, h, y, h_next, rows, L);
 }
 
 }  // namespace wbmm
