@@ -120,13 +120,16 @@ def _p(t):
         return None
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("WBMM tensors must be contiguous CUDA tensors")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream, ref=None):
     """Stream handle for a call whose maps live on ``ref``'s device.  The
     library launches on the current device, so ``ref`` and the stream must
     be on it."""
+    if stream is None and ref is not None and ref.get_device() == torch.cuda.current_device():
+        # the current device's current stream, without the stream object
+        return torch._C._cuda_getCurrentRawStream(ref.get_device())
     s = torch.cuda.current_stream() if stream is None else stream
     if ref is not None:
         d, cur = ref.get_device(), torch.cuda.current_device()
@@ -134,15 +137,16 @@ def _stream(stream, ref=None):
             raise WbmmError(WBMM_ERR_INVALID_ARG,
                             "maps on cuda:%d, stream on cuda:%d, current device cuda:%d"
                             % (d, s.device_index, cur))
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _need(name, t, numel, ref, dtype=None):
     """Buffer ``t`` (optional) must sit on ``ref``'s device, have ``ref``'s
     dtype (or ``dtype``) and hold at least ``numel`` elements."""
+    if t is None:
+        return
     want = dtype or ref.dtype
-    if t is None or (t.dtype is want and t.numel() >= numel
-                     and t.get_device() == ref.get_device()):
+    if t.dtype is want and t.numel() >= numel and t.get_device() == ref.get_device():
         return
     if t.get_device() != ref.get_device():
         raise WbmmError(WBMM_ERR_INVALID_ARG, "%s is on %s, the map on %s"
@@ -169,9 +173,12 @@ def _windows(B, C, H, W, w):
 
 
 def _seq_shape(v):
-    if v.dim() < 2:
+    shape = v.shape
+    if len(shape) == 3:
+        return shape
+    if len(shape) < 2:
         raise ValueError("recurrence tensors must be [B, C, L], [B, C, H, W] or [B, C]")
-    return int(v.shape[0]), int(v.shape[1]), math.prod(int(n) for n in v.shape[2:])
+    return shape[0], shape[1], math.prod(shape[2:])
 
 
 def _need_seq(ref, B, C, L, h0, hT, lengths, states, codes=(), exps=()):

@@ -2,7 +2,15 @@
 // channel, codes in window order ([C][windows][w*w], windows in (b, i, j)
 // order), so that a run of windows of one channel is one contiguous run of
 // bytes for the table gradient that reads them.
+//
+// Bands (the w image rows of one window row of a plane) follow each other in
+// the map, and a band's windows follow each other in the codes, so both
+// directions move whole bands with contiguous accesses and permute within a
+// band in shared memory: a block takes the next few bands, one thread a window
+// row.  Bound by memory: 3 bytes an element in bf16 and 5 in fp32.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "ckpt_common.cuh"
 #include "ptx_sm100.cuh"
@@ -28,7 +36,7 @@ __device__ __forceinline__ long long window_base(long long n, int c, int C, int 
     return ((b * C + c) * H + (long long)i * w) * W + (long long)j * w;
 }
 
-// One warp per window.
+// One warp per window: bands beyond the block kernels' shared memory.
 template <typename T>
 __global__ void ckpt_store_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes,
                                   uint8_t* __restrict__ exps, int C, int H, int W, int w, int nh,
@@ -87,6 +95,280 @@ __global__ void ckpt_restore_kernel(const uint8_t* __restrict__ codes,
     }
 }
 
+// ------------------------------------------------------------ block kernels
+constexpr int kBandThreads = 256;
+constexpr int kBandElems = 8192;        // elements of a block's bands, at most
+
+struct BandArgs {
+    int B, C, nh, nw, w, W;
+    int nb;                 // bands a block
+    long long bands;        // of all planes
+    unsigned div_row;       // ceil(2^32 / (nw w)) and / nw, 0 for a divisor of 1
+    unsigned div_nw;
+};
+
+// n / d for n d < 2^32, m = ceil(2^32 / d).
+__device__ __forceinline__ int fast_div(int n, unsigned m)
+{
+    return m ? (int)__umulhi((unsigned)n, m) : n;
+}
+
+// A window row of the block's bands.
+struct WinRow {
+    int band, r, j;
+    __device__ __forceinline__ WinRow(const BandArgs& P, int k)
+    {
+        band = fast_div(k, P.div_row);
+        const int in = k - band * P.nw * P.w;
+        r = fast_div(in, P.div_nw);
+        j = in - r * P.nw;
+    }
+};
+
+// First window of the block's band k, in checkpoint order.
+__device__ __forceinline__ long long band_window(const BandArgs& P, long long f)
+{
+    const long long plane = f / P.nh;
+    const int i = (int)(f - plane * P.nh);
+    const long long b = plane / P.C, c = plane - b * P.C;
+    return ((c * P.B + b) * P.nh + i) * P.nw;
+}
+
+// WS: the window size where it is known at compile time (0: w as given); EVEN:
+// w is even (and so W), values move in pairs.
+template <typename T, int WS, bool EVEN>
+__global__ void __launch_bounds__(kBandThreads)
+    ckpt_store_bands_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes,
+                            uint8_t* __restrict__ exps, const BandArgs P)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int w = WS ? WS : P.w, tid = threadIdx.x;
+    const int bn = w * P.W;                                 // elements a band
+    const long long f0 = (long long)blockIdx.x * P.nb;
+    const int nb = (int)(P.bands - f0 < P.nb ? P.bands - f0 : P.nb);
+    const int windows = nb * P.nw, rows = windows * w;
+    // the map's elements, with their offset from a 16-byte boundary; codes;
+    // the windows' largest magnitudes
+    uint8_t* img = smem;
+    uint8_t* cds = smem + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
+    uint32_t* top = reinterpret_cast<uint32_t*>(cds + (P.nb * bn + 15) / 16 * 16);
+    for (int k = tid; k < windows; k += kBandThreads)
+        top[k] = 0u;
+    grid_dep_wait();
+    grid_dep_launch();
+    const T* src = x + f0 * bn;
+    const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+    {
+        const uint8_t* at = reinterpret_cast<const uint8_t*>(src);
+        const uint8_t* end = at + (long long)nb * bn * (int)sizeof(T);
+        for (const uint8_t* p = at - off + 16 * tid; p < end; p += 16 * kBandThreads) {
+            const uint32_t to = smem_u32(img + (p - (at - off)));
+            if (p >= at && p + 16 <= end) {
+                cp_async_16z(to, p, 16u);
+            } else {
+                // the block's first and last partial 16 bytes, by elements
+                for (int q = 0; q < 16; q += (int)sizeof(T))
+                    if (p + q >= at && p + q < end)
+                        *reinterpret_cast<T*>(img + (p + q - (at - off))) =
+                            *reinterpret_cast<const T*>(p + q);
+            }
+        }
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    const T* map = reinterpret_cast<const T*>(img + off);
+    for (int k = tid; k < rows; k += kBandThreads) {
+        const WinRow q(P, k);
+        const T* e = map + q.band * bn + q.r * P.W + q.j * w;
+        uint32_t m = 0;
+        if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+            for (int t = 0; t < w; ++t)
+                m = max(m, __float_as_uint(e[t]) & kAbsMask);
+        } else if constexpr (EVEN) {
+#pragma unroll
+            for (int t = 0; t < w / 2; ++t)
+                m = __vmaxu2(m, reinterpret_cast<const uint32_t*>(e)[t] & 0x7fff7fffu);
+            m = max(m & 0xffff0000u, m << 16);
+        } else {
+#pragma unroll
+            for (int t = 0; t < w; ++t)
+                m = max(m, (uint32_t)(reinterpret_cast<const uint16_t*>(e)[t] & 0x7fffu) << 16);
+        }
+        atomicMax(&top[q.band * P.nw + q.j], m);
+    }
+    __syncthreads();
+    for (int k = tid; k < rows; k += kBandThreads) {
+        const WinRow q(P, k);
+        const T* e = map + q.band * bn + q.r * P.W + q.j * w;
+        const uint32_t ex = group_exp(top[q.band * P.nw + q.j]);
+        const float inv = inv_step_of(ex);
+        uint8_t* d = cds + q.band * bn + (q.j * w + q.r) * w;
+        if (ex >= kExpTop) {
+            for (int t = 0; t < w; ++t)
+                d[t] = (uint8_t)quant_code(group_fix(ld_f(e + t), ex), inv);
+        } else if constexpr (EVEN) {
+#pragma unroll
+            for (int t = 0; t < w / 2; ++t) {
+                float a, b;
+                if constexpr (std::is_same<T, float>::value) {
+                    a = e[2 * t];
+                    b = e[2 * t + 1];
+                } else {
+                    const uint32_t u = reinterpret_cast<const uint32_t*>(e)[t];
+                    a = __uint_as_float(u << 16);
+                    b = __uint_as_float(u & 0xffff0000u);
+                }
+                reinterpret_cast<uint16_t*>(d)[t] =
+                    (uint16_t)__byte_perm(quant_code(a, inv), quant_code(b, inv), 0x0040);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < w; ++t)
+                d[t] = (uint8_t)quant_code(ld_f(e + t), inv);
+        }
+    }
+    __syncthreads();
+    const int d2 = w * w;
+    for (int band = tid / 32; band < nb; band += kBandThreads / 32) {
+        const int lane = tid & 31;
+        const long long n = band_window(P, f0 + band);
+        uint8_t* out = codes + n * d2;
+        const uint8_t* in = cds + band * bn;
+        if (bn % 4 == 0) {
+            for (int k = lane; k < bn / 4; k += 32)
+                reinterpret_cast<uint32_t*>(out)[k] = reinterpret_cast<const uint32_t*>(in)[k];
+        } else {
+            for (int k = lane; k < bn; k += 32)
+                out[k] = in[k];
+        }
+        for (int k = lane; k < P.nw; k += 32)
+            exps[n + k] = (uint8_t)group_exp(top[band * P.nw + k]);
+    }
+}
+
+template <typename T, int WS, bool EVEN>
+__global__ void __launch_bounds__(kBandThreads)
+    ckpt_restore_bands_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps,
+                              T* __restrict__ x, const BandArgs P)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int w = WS ? WS : P.w, tid = threadIdx.x;
+    const int bn = w * P.W, d2 = w * w;
+    const long long f0 = (long long)blockIdx.x * P.nb;
+    const int nb = (int)(P.bands - f0 < P.nb ? P.bands - f0 : P.nb);
+    const int windows = nb * P.nw, rows = windows * w;
+    uint8_t* img = smem;
+    uint8_t* cds = smem + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
+    float* step = reinterpret_cast<float*>(cds + (P.nb * bn + 15) / 16 * 16);
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int band = tid / 32; band < nb; band += kBandThreads / 32) {
+        const int lane = tid & 31;
+        const long long n = band_window(P, f0 + band);
+        const uint8_t* in = codes + n * d2;
+        uint8_t* to = cds + band * bn;
+        if (bn % 8 == 0) {
+            for (int k = lane; k < bn / 8; k += 32)
+                cp_async_8(smem_u32(to + 8 * k), in + 8 * k);
+        } else if (bn % 4 == 0) {
+            for (int k = lane; k < bn / 4; k += 32)
+                cp_async_4(smem_u32(to + 4 * k), in + 4 * k);
+        } else {
+            for (int k = lane; k < bn; k += 32)
+                to[k] = in[k];
+        }
+        for (int k = lane; k < P.nw; k += 32)
+            step[band * P.nw + k] = step_of(exps[n + k]);
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    T* dst = x + f0 * bn;
+    const int off = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
+    T* map = reinterpret_cast<T*>(img + off);
+    for (int k = tid; k < rows; k += kBandThreads) {
+        const WinRow q(P, k);
+        T* e = map + q.band * bn + q.r * P.W + q.j * w;
+        const float st = step[q.band * P.nw + q.j];
+        const uint8_t* c = cds + q.band * bn + (q.j * w + q.r) * w;
+        if constexpr (EVEN) {
+#pragma unroll
+            for (int t = 0; t < w / 2; ++t) {
+                const uint32_t u = reinterpret_cast<const uint16_t*>(c)[t];
+                const float a = code_value(u & 0xffu, st), b = code_value(u >> 8, st);
+                if constexpr (std::is_same<T, float>::value) {
+                    e[2 * t] = a;
+                    e[2 * t + 1] = b;
+                } else {
+                    // exact in bf16: the upper halves
+                    reinterpret_cast<uint32_t*>(e)[t] =
+                        __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < w; ++t)
+                st_f(e + t, code_value(c[t], st));
+        }
+    }
+    __syncthreads();
+    uint8_t* at = reinterpret_cast<uint8_t*>(dst);
+    uint8_t* end = at + (long long)nb * bn * (int)sizeof(T);
+    for (uint8_t* p = at - off + 16 * tid; p < end; p += 16 * kBandThreads) {
+        const uint8_t* from = img + (p - (at - off));
+        if (p >= at && p + 16 <= end) {
+            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(from);
+        } else {
+            for (int q = 0; q < 16; q += (int)sizeof(T))
+                if (p + q >= at && p + q < end)
+                    *reinterpret_cast<T*>(p + q) = *reinterpret_cast<const T*>(from + q);
+        }
+    }
+}
+
+unsigned ceil_recip(int d) { return d == 1 ? 0u : (unsigned)(((1ull << 32) + d - 1) / d); }
+
+// The block kernels' arguments: as many bands a block as give each thread a
+// window row.  False where a band does not fit.
+bool band_args(const Geom& g, size_t sz, BandArgs* P, size_t* smem)
+{
+    const long long bn = (long long)g.w * g.W;
+    if (bn > kBandElems)
+        return false;
+    P->B = g.B; P->C = g.C; P->nh = g.nh; P->nw = g.nw; P->w = g.w; P->W = g.W;
+    P->bands = g.bands * g.C;
+    const int rows = g.nw * g.w;
+    long long nb = kBandThreads / rows;
+    nb = nb < 1 ? 1 : nb > kBandElems / bn ? kBandElems / bn : nb;
+    P->nb = (int)nb;
+    P->div_row = ceil_recip(rows);
+    P->div_nw = ceil_recip(g.nw);
+    *smem = (nb * bn * sz + 31) / 16 * 16 + (nb * bn + 15) / 16 * 16 + (size_t)nb * g.nw * 4;
+    return *smem <= 48 * 1024 && (P->bands + nb - 1) / nb < (1ll << 31);
+}
+
+// KernelT<T, WS, EVEN>::run for the window size.
+template <template <typename, int, bool> class KernelT, typename T, typename... Args>
+cudaError_t band_launch(const BandArgs& P, size_t smem, const Launch& L, Args... args)
+{
+    auto kernel = P.w == 14 ? KernelT<T, 14, true>::get()
+                  : P.w == 7 ? KernelT<T, 7, false>::get()
+                  : P.w % 2 == 0 ? KernelT<T, 0, true>::get()
+                                 : KernelT<T, 0, false>::get();
+    const dim3 grid((unsigned)((P.bands + P.nb - 1) / P.nb)), block(kBandThreads);
+    return launch_pdl(kernel, grid, block, smem, L.stream, args..., P);
+}
+
+template <typename T, int WS, bool EVEN>
+struct StoreKernel {
+    static constexpr auto get() { return &ckpt_store_bands_kernel<T, WS, EVEN>; }
+};
+
+template <typename T, int WS, bool EVEN>
+struct RestoreKernel {
+    static constexpr auto get() { return &ckpt_restore_bands_kernel<T, WS, EVEN>; }
+};
+
 unsigned warp_grid(long long warps, const Launch& L)
 {
     const long long blocks = (warps + 3) / 4, most = (long long)L.num_sms * 16;
@@ -98,10 +380,18 @@ unsigned warp_grid(long long warps, const Launch& L)
 cudaError_t checkpoint_launch(const Geom& g, bool is_bf16, const void* x, uint8_t* codes,
                               uint8_t* exps, const Launch& L)
 {
+    BandArgs P;
+    size_t smem;
+    cudaError_t e;
     const long long nwin = g.bands * g.nw;
     const dim3 grid(warp_grid(nwin * g.C, L)), block(128);
-    cudaError_t e =
-        is_bf16 ? launch_pdl(ckpt_store_kernel<__nv_bfloat16>, grid, block, 0, L.stream,
+    if (band_args(g, is_bf16 ? 2 : 4, &P, &smem))
+        e = is_bf16 ? band_launch<StoreKernel, __nv_bfloat16>(
+                          P, smem, L, static_cast<const __nv_bfloat16*>(x), codes, exps)
+                    : band_launch<StoreKernel, float>(P, smem, L, static_cast<const float*>(x), codes,
+                                                      exps);
+    else
+        e = is_bf16 ? launch_pdl(ckpt_store_kernel<__nv_bfloat16>, grid, block, 0, L.stream,
                              static_cast<const __nv_bfloat16*>(x), codes, exps, g.C, g.H, g.W, g.w,
                              g.nh, g.nw, nwin)
                 : launch_pdl(ckpt_store_kernel<float>, grid, block, 0, L.stream,
@@ -116,10 +406,18 @@ cudaError_t checkpoint_launch(const Geom& g, bool is_bf16, const void* x, uint8_
 cudaError_t checkpoint_restore_launch(const Geom& g, bool is_bf16, const uint8_t* codes,
                                       const uint8_t* exps, void* x, const Launch& L)
 {
+    BandArgs P;
+    size_t smem;
+    cudaError_t e;
     const long long nwin = g.bands * g.nw;
     const dim3 grid(warp_grid(nwin * g.C, L)), block(128);
-    cudaError_t e =
-        is_bf16 ? launch_pdl(ckpt_restore_kernel<__nv_bfloat16>, grid, block, 0, L.stream, codes,
+    if (band_args(g, is_bf16 ? 2 : 4, &P, &smem))
+        e = is_bf16 ? band_launch<RestoreKernel, __nv_bfloat16>(P, smem, L, codes, exps,
+                                                                static_cast<__nv_bfloat16*>(x))
+                    : band_launch<RestoreKernel, float>(P, smem, L, codes, exps,
+                                                        static_cast<float*>(x));
+    else
+        e = is_bf16 ? launch_pdl(ckpt_restore_kernel<__nv_bfloat16>, grid, block, 0, L.stream, codes,
                              exps, static_cast<__nv_bfloat16*>(x), g.C, g.H, g.W, g.w, g.nh, g.nw,
                              nwin)
                 : launch_pdl(ckpt_restore_kernel<float>, grid, block, 0, L.stream, codes, exps,
