@@ -102,7 +102,7 @@ constexpr int kBandElems = 8192;        // elements of a block's bands, at most
 struct BandArgs {
     int B, C, nh, nw, w, W;
     int nb;                 // bands a block
-    long long bands;        // of all planes
+    unsigned bands;         // of all planes
     unsigned div_row;       // ceil(2^32 / (nw w)) and / nw, 0 for a divisor of 1
     unsigned div_nw;
 };
@@ -125,13 +125,12 @@ struct WinRow {
     }
 };
 
-// First window of the block's band k, in checkpoint order.
-__device__ __forceinline__ long long band_window(const BandArgs& P, long long f)
+// The band's place among the bands in checkpoint order (channels first).
+__device__ __forceinline__ unsigned band_place(const BandArgs& P, unsigned f)
 {
-    const long long plane = f / P.nh;
-    const int i = (int)(f - plane * P.nh);
-    const long long b = plane / P.C, c = plane - b * P.C;
-    return ((c * P.B + b) * P.nh + i) * P.nw;
+    const unsigned plane = f / (unsigned)P.nh, i = f - plane * P.nh;
+    const unsigned b = plane / (unsigned)P.C, c = plane - b * P.C;
+    return (c * P.B + b) * P.nh + i;
 }
 
 // WS: the window size where it is known at compile time (0: w as given); EVEN:
@@ -144,19 +143,22 @@ __global__ void __launch_bounds__(kBandThreads)
     extern __shared__ __align__(16) uint8_t smem[];
     const int w = WS ? WS : P.w, tid = threadIdx.x;
     const int bn = w * P.W;                                 // elements a band
-    const long long f0 = (long long)blockIdx.x * P.nb;
-    const int nb = (int)(P.bands - f0 < P.nb ? P.bands - f0 : P.nb);
+    const unsigned f0 = blockIdx.x * (unsigned)P.nb;
+    const int nb = (int)min(P.bands - f0, (unsigned)P.nb);
     const int windows = nb * P.nw, rows = windows * w;
     // the map's elements, with their offset from a 16-byte boundary; codes;
     // the windows' largest magnitudes
     uint8_t* img = smem;
     uint8_t* cds = smem + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
     uint32_t* top = reinterpret_cast<uint32_t*>(cds + (P.nb * bn + 15) / 16 * 16);
+    unsigned* place = reinterpret_cast<unsigned*>(top + P.nb * P.nw);
+    for (int k = tid; k < nb; k += kBandThreads)
+        place[k] = band_place(P, f0 + k);
     for (int k = tid; k < windows; k += kBandThreads)
         top[k] = 0u;
     grid_dep_wait();
     grid_dep_launch();
-    const T* src = x + f0 * bn;
+    const T* src = x + (long long)f0 * bn;
     const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
     {
         const uint8_t* at = reinterpret_cast<const uint8_t*>(src);
@@ -229,13 +231,15 @@ __global__ void __launch_bounds__(kBandThreads)
         }
     }
     __syncthreads();
-    const int d2 = w * w;
     for (int band = tid / 32; band < nb; band += kBandThreads / 32) {
         const int lane = tid & 31;
-        const long long n = band_window(P, f0 + band);
-        uint8_t* out = codes + n * d2;
+        const unsigned n = place[band];
+        uint8_t* out = codes + (long long)n * bn;
         const uint8_t* in = cds + band * bn;
-        if (bn % 4 == 0) {
+        if (bn % 8 == 0) {
+            for (int k = lane; k < bn / 8; k += 32)
+                reinterpret_cast<uint2*>(out)[k] = reinterpret_cast<const uint2*>(in)[k];
+        } else if (bn % 4 == 0) {
             for (int k = lane; k < bn / 4; k += 32)
                 reinterpret_cast<uint32_t*>(out)[k] = reinterpret_cast<const uint32_t*>(in)[k];
         } else {
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kBandThreads)
                 out[k] = in[k];
         }
         for (int k = lane; k < P.nw; k += 32)
-            exps[n + k] = (uint8_t)group_exp(top[band * P.nw + k]);
+            exps[(long long)n * P.nw + k] = (uint8_t)group_exp(top[band * P.nw + k]);
     }
 }
 
@@ -254,19 +258,23 @@ __global__ void __launch_bounds__(kBandThreads)
 {
     extern __shared__ __align__(16) uint8_t smem[];
     const int w = WS ? WS : P.w, tid = threadIdx.x;
-    const int bn = w * P.W, d2 = w * w;
-    const long long f0 = (long long)blockIdx.x * P.nb;
-    const int nb = (int)(P.bands - f0 < P.nb ? P.bands - f0 : P.nb);
+    const int bn = w * P.W;
+    const unsigned f0 = blockIdx.x * (unsigned)P.nb;
+    const int nb = (int)min(P.bands - f0, (unsigned)P.nb);
     const int windows = nb * P.nw, rows = windows * w;
     uint8_t* img = smem;
     uint8_t* cds = smem + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
     float* step = reinterpret_cast<float*>(cds + (P.nb * bn + 15) / 16 * 16);
+    unsigned* place = reinterpret_cast<unsigned*>(step + P.nb * P.nw);
+    for (int k = tid; k < nb; k += kBandThreads)
+        place[k] = band_place(P, f0 + k);
+    __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
     for (int band = tid / 32; band < nb; band += kBandThreads / 32) {
         const int lane = tid & 31;
-        const long long n = band_window(P, f0 + band);
-        const uint8_t* in = codes + n * d2;
+        const unsigned n = place[band];
+        const uint8_t* in = codes + (long long)n * bn;
         uint8_t* to = cds + band * bn;
         if (bn % 8 == 0) {
             for (int k = lane; k < bn / 8; k += 32)
@@ -279,11 +287,11 @@ __global__ void __launch_bounds__(kBandThreads)
                 to[k] = in[k];
         }
         for (int k = lane; k < P.nw; k += 32)
-            step[band * P.nw + k] = step_of(exps[n + k]);
+            step[band * P.nw + k] = step_of(exps[(long long)n * P.nw + k]);
     }
     cp_async_wait_all();
     __syncthreads();
-    T* dst = x + f0 * bn;
+    T* dst = x + (long long)f0 * bn;
     const int off = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
     T* map = reinterpret_cast<T*>(img + off);
     for (int k = tid; k < rows; k += kBandThreads) {
@@ -336,15 +344,17 @@ bool band_args(const Geom& g, size_t sz, BandArgs* P, size_t* smem)
     if (bn > kBandElems)
         return false;
     P->B = g.B; P->C = g.C; P->nh = g.nh; P->nw = g.nw; P->w = g.w; P->W = g.W;
-    P->bands = g.bands * g.C;
+    if (g.bands * g.C >= (1ll << 31))
+        return false;
+    P->bands = (unsigned)(g.bands * g.C);
     const int rows = g.nw * g.w;
     long long nb = kBandThreads / rows;
     nb = nb < 1 ? 1 : nb > kBandElems / bn ? kBandElems / bn : nb;
     P->nb = (int)nb;
     P->div_row = ceil_recip(rows);
     P->div_nw = ceil_recip(g.nw);
-    *smem = (nb * bn * sz + 31) / 16 * 16 + (nb * bn + 15) / 16 * 16 + (size_t)nb * g.nw * 4;
-    return *smem <= 48 * 1024 && (P->bands + nb - 1) / nb < (1ll << 31);
+    *smem = (nb * bn * sz + 31) / 16 * 16 + (nb * bn + 15) / 16 * 16 + (size_t)nb * (g.nw + 1) * 4;
+    return *smem <= 48 * 1024;
 }
 
 // KernelT<T, WS, EVEN>::run for the window size.
