@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "ckpt_common.cuh"
+#include "f32x2.cuh"
 #include "ptx_sm100.cuh"
 #include "wbmm_internal.h"
 
@@ -97,6 +98,7 @@ __global__ void ckpt_restore_kernel(const uint8_t* __restrict__ codes,
 
 // ------------------------------------------------------------ block kernels
 constexpr int kBandThreads = 256;
+constexpr int kBandRows = 2;            // window rows a thread, at most (WS > 0)
 constexpr int kBandElems = 8192;        // elements of a block's bands, at most
 
 struct BandArgs {
@@ -133,9 +135,123 @@ __device__ __forceinline__ unsigned band_place(const BandArgs& P, unsigned f)
     return (c * P.B + b) * P.nh + i;
 }
 
-// WS: the window size where it is known at compile time (0: w as given); EVEN:
-// w is even (and so W), values move in pairs.
-template <typename T, int WS, bool EVEN>
+// The WS values of a window row.  bf16 rows start at an even or an odd
+// element: of an odd one the words from the element before are read (within
+// the image, which has room in front) and shifted.
+template <typename T, int WS>
+struct RowVals {
+    static constexpr bool F32 = std::is_same<T, float>::value;
+    static constexpr int N = F32 ? WS : (WS + 1) / 2;
+    uint32_t u[N];      // fp32 bits, or bf16 pairs (a last odd half is zero)
+
+    __device__ __forceinline__ void load(const T* e)
+    {
+        if constexpr (F32) {
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+                u[t] = __float_as_uint(e[t]);
+        } else if constexpr (WS % 2 == 0) {
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+                u[t] = reinterpret_cast<const uint32_t*>(e)[t];
+        } else {
+            const bool odd = reinterpret_cast<uintptr_t>(e) & 2;
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(e - (odd ? 1 : 0));
+#pragma unroll
+            for (int t = 0; t < N; ++t)
+                u[t] = p[t];
+            if (odd) {
+#pragma unroll
+                for (int t = 0; t + 1 < N; ++t)
+                    u[t] = __funnelshift_r(u[t], u[t + 1], 16);
+                u[N - 1] >>= 16;
+            }
+            u[N - 1] &= 0xffffu;
+        }
+    }
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+            m = F32 ? max(m, u[t] & kAbsMask) : __vmaxu2(m, u[t] & 0x7fff7fffu);
+        return F32 ? m : max(m & 0xffff0000u, m << 16);
+    }
+    __device__ __forceinline__ float value(int t) const
+    {
+        if constexpr (F32)
+            return __uint_as_float(u[t]);
+        else
+            return __uint_as_float(t & 1 ? u[t / 2] & 0xffff0000u : u[t / 2] << 16);
+    }
+    // group_fix of every value: exact in bf16 too (127 steps are)
+    __device__ __forceinline__ void fix(uint32_t e)
+    {
+#pragma unroll
+        for (int t = 0; t < WS; ++t) {
+            const uint32_t b = __float_as_uint(group_fix(value(t), e));
+            if constexpr (F32)
+                u[t] = b;
+            else
+                u[t / 2] = t & 1 ? (u[t / 2] & 0xffffu) | (b & 0xffff0000u)
+                                 : (u[t / 2] & 0xffff0000u) | (b >> 16);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* d, float inv) const
+    {
+#pragma unroll
+        for (int t = 0; t < WS; t += 2) {
+            const F2 q = fma2({value(t), t + 1 < WS ? value(t + 1) : 0.0f}, {inv, inv},
+                              {12583040.0f, 12583040.0f});
+            const uint32_t a = __float_as_uint(q.x), b = __float_as_uint(q.y);
+            if constexpr (WS % 2 == 0) {
+                reinterpret_cast<uint16_t*>(d)[t / 2] = (uint16_t)__byte_perm(a, b, 0x0040);
+            } else {
+                d[t] = (uint8_t)a;
+                if (t + 1 < WS)
+                    d[t + 1] = (uint8_t)b;
+            }
+        }
+    }
+};
+
+template <typename T, int WS>
+__device__ __forceinline__ void restore_row(T* e, const uint8_t* c, float st)
+{
+    constexpr bool F32 = std::is_same<T, float>::value;
+#pragma unroll
+    for (int t = 0; t < WS; t += 2) {
+        uint32_t a, b;
+        if constexpr (WS % 2 == 0) {
+            const uint32_t u = reinterpret_cast<const uint16_t*>(c)[t / 2];
+            a = __byte_perm(u, 0x4b000000u, 0x7440);
+            b = __byte_perm(u, 0x4b000000u, 0x7441);
+        } else {
+            a = 0x4b000000u | c[t];
+            b = t + 1 < WS ? 0x4b000000u | c[t + 1] : a;
+        }
+        // 2^23 + code, less 2^23 + 128, times the step: all exact
+        const F2 v = mul2(add2({__uint_as_float(a), __uint_as_float(b)}, {-8388736.0f, -8388736.0f}),
+                          {st, st});
+        if constexpr (F32) {
+            e[t] = v.x;
+            if (t + 1 < WS)
+                e[t + 1] = v.y;
+        } else if constexpr (WS % 2 == 0) {
+            // exact in bf16: the upper halves
+            reinterpret_cast<uint32_t*>(e)[t / 2] =
+                __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+        } else {
+            reinterpret_cast<uint16_t*>(e)[t] = (uint16_t)(__float_as_uint(v.x) >> 16);
+            if (t + 1 < WS)
+                reinterpret_cast<uint16_t*>(e)[t + 1] = (uint16_t)(__float_as_uint(v.y) >> 16);
+        }
+    }
+}
+
+// WS: the window size, 2 to 16 as the tensor-core kernels compile for, or 0
+// for any other (w as given).
+template <typename T, int WS>
 __global__ void __launch_bounds__(kBandThreads)
     ckpt_store_bands_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes,
                             uint8_t* __restrict__ exps, const BandArgs P)
@@ -148,8 +264,8 @@ __global__ void __launch_bounds__(kBandThreads)
     const int windows = nb * P.nw, rows = windows * w;
     // the map's elements, with their offset from a 16-byte boundary; codes;
     // the windows' largest magnitudes
-    uint8_t* img = smem;
-    uint8_t* cds = smem + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
+    uint8_t* img = smem + 16;
+    uint8_t* cds = img + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
     uint32_t* top = reinterpret_cast<uint32_t*>(cds + (P.nb * bn + 15) / 16 * 16);
     unsigned* place = reinterpret_cast<unsigned*>(top + P.nb * P.nw);
     for (int k = tid; k < nb; k += kBandThreads)
@@ -179,55 +295,53 @@ __global__ void __launch_bounds__(kBandThreads)
     cp_async_wait_all();
     __syncthreads();
     const T* map = reinterpret_cast<const T*>(img + off);
-    for (int k = tid; k < rows; k += kBandThreads) {
-        const WinRow q(P, k);
-        const T* e = map + q.band * bn + q.r * P.W + q.j * w;
-        uint32_t m = 0;
-        if constexpr (std::is_same<T, float>::value) {
+    if constexpr (WS > 0) {
+        // each thread's window rows stay in registers between the two passes
+        RowVals<T, WS> val[kBandRows];
+        int win[kBandRows], at[kBandRows];
 #pragma unroll
-            for (int t = 0; t < w; ++t)
-                m = max(m, __float_as_uint(e[t]) & kAbsMask);
-        } else if constexpr (EVEN) {
-#pragma unroll
-            for (int t = 0; t < w / 2; ++t)
-                m = __vmaxu2(m, reinterpret_cast<const uint32_t*>(e)[t] & 0x7fff7fffu);
-            m = max(m & 0xffff0000u, m << 16);
-        } else {
-#pragma unroll
-            for (int t = 0; t < w; ++t)
-                m = max(m, (uint32_t)(reinterpret_cast<const uint16_t*>(e)[t] & 0x7fffu) << 16);
-        }
-        atomicMax(&top[q.band * P.nw + q.j], m);
-    }
-    __syncthreads();
-    for (int k = tid; k < rows; k += kBandThreads) {
-        const WinRow q(P, k);
-        const T* e = map + q.band * bn + q.r * P.W + q.j * w;
-        const uint32_t ex = group_exp(top[q.band * P.nw + q.j]);
-        const float inv = inv_step_of(ex);
-        uint8_t* d = cds + q.band * bn + (q.j * w + q.r) * w;
-        if (ex >= kExpTop) {
-            for (int t = 0; t < w; ++t)
-                d[t] = (uint8_t)quant_code(group_fix(ld_f(e + t), ex), inv);
-        } else if constexpr (EVEN) {
-#pragma unroll
-            for (int t = 0; t < w / 2; ++t) {
-                float a, b;
-                if constexpr (std::is_same<T, float>::value) {
-                    a = e[2 * t];
-                    b = e[2 * t + 1];
-                } else {
-                    const uint32_t u = reinterpret_cast<const uint32_t*>(e)[t];
-                    a = __uint_as_float(u << 16);
-                    b = __uint_as_float(u & 0xffff0000u);
-                }
-                reinterpret_cast<uint16_t*>(d)[t] =
-                    (uint16_t)__byte_perm(quant_code(a, inv), quant_code(b, inv), 0x0040);
+        for (int m = 0; m < kBandRows; ++m) {
+            const int k = tid + m * kBandThreads;
+            if (k < rows) {
+                const WinRow q(P, k);
+                win[m] = q.band * P.nw + q.j;
+                at[m] = q.band * bn + (q.j * WS + q.r) * WS;
+                val[m].load(map + q.band * bn + q.r * P.W + q.j * WS);
+                atomicMax(&top[win[m]], val[m].top());
             }
-        } else {
+        }
+        __syncthreads();
 #pragma unroll
+        for (int m = 0; m < kBandRows; ++m) {
+            if (tid + m * kBandThreads < rows) {
+                const uint32_t ex = group_exp(top[win[m]]);
+                if (ex >= kExpTop)
+                    val[m].fix(ex);
+                val[m].store(cds + at[m], inv_step_of(ex));
+            }
+        }
+    } else {
+        for (int k = tid; k < rows; k += kBandThreads) {
+            const WinRow q(P, k);
+            const T* e = map + q.band * bn + q.r * P.W + q.j * w;
+            uint32_t m = 0;
             for (int t = 0; t < w; ++t)
-                d[t] = (uint8_t)quant_code(ld_f(e + t), inv);
+                m = max(m, __float_as_uint(ld_f(e + t)) & kAbsMask);
+            atomicMax(&top[q.band * P.nw + q.j], m);
+        }
+        __syncthreads();
+        for (int k = tid; k < rows; k += kBandThreads) {
+            const WinRow q(P, k);
+            const T* e = map + q.band * bn + q.r * P.W + q.j * w;
+            const uint32_t ex = group_exp(top[q.band * P.nw + q.j]);
+            const float inv = inv_step_of(ex);
+            uint8_t* d = cds + q.band * bn + (q.j * w + q.r) * w;
+            for (int t = 0; t < w; ++t) {
+                float v = ld_f(e + t);
+                if (ex >= kExpTop)
+                    v = group_fix(v, ex);
+                d[t] = (uint8_t)quant_code(v, inv);
+            }
         }
     }
     __syncthreads();
@@ -251,7 +365,7 @@ __global__ void __launch_bounds__(kBandThreads)
     }
 }
 
-template <typename T, int WS, bool EVEN>
+template <typename T, int WS>
 __global__ void __launch_bounds__(kBandThreads)
     ckpt_restore_bands_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps,
                               T* __restrict__ x, const BandArgs P)
@@ -262,8 +376,8 @@ __global__ void __launch_bounds__(kBandThreads)
     const unsigned f0 = blockIdx.x * (unsigned)P.nb;
     const int nb = (int)min(P.bands - f0, (unsigned)P.nb);
     const int windows = nb * P.nw, rows = windows * w;
-    uint8_t* img = smem;
-    uint8_t* cds = smem + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
+    uint8_t* img = smem + 16;
+    uint8_t* cds = img + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
     float* step = reinterpret_cast<float*>(cds + (P.nb * bn + 15) / 16 * 16);
     unsigned* place = reinterpret_cast<unsigned*>(step + P.nb * P.nw);
     for (int k = tid; k < nb; k += kBandThreads)
@@ -299,22 +413,9 @@ __global__ void __launch_bounds__(kBandThreads)
         T* e = map + q.band * bn + q.r * P.W + q.j * w;
         const float st = step[q.band * P.nw + q.j];
         const uint8_t* c = cds + q.band * bn + (q.j * w + q.r) * w;
-        if constexpr (EVEN) {
-#pragma unroll
-            for (int t = 0; t < w / 2; ++t) {
-                const uint32_t u = reinterpret_cast<const uint16_t*>(c)[t];
-                const float a = code_value(u & 0xffu, st), b = code_value(u >> 8, st);
-                if constexpr (std::is_same<T, float>::value) {
-                    e[2 * t] = a;
-                    e[2 * t + 1] = b;
-                } else {
-                    // exact in bf16: the upper halves
-                    reinterpret_cast<uint32_t*>(e)[t] =
-                        __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-                }
-            }
+        if constexpr (WS > 0) {
+            restore_row<T, WS>(e, c, st);
         } else {
-#pragma unroll
             for (int t = 0; t < w; ++t)
                 st_f(e + t, code_value(c[t], st));
         }
@@ -336,9 +437,8 @@ __global__ void __launch_bounds__(kBandThreads)
 
 unsigned ceil_recip(int d) { return d == 1 ? 0u : (unsigned)(((1ull << 32) + d - 1) / d); }
 
-// The block kernels' arguments: as many bands a block as give each thread a
-// window row.  False where a band does not fit.
-bool band_args(const Geom& g, size_t sz, BandArgs* P, size_t* smem)
+// The block kernels' arguments; false where a band does not fit.
+bool band_args(const Geom& g, size_t sz, int num_sms, BandArgs* P, size_t* smem)
 {
     const long long bn = (long long)g.w * g.W;
     if (bn > kBandElems)
@@ -348,35 +448,44 @@ bool band_args(const Geom& g, size_t sz, BandArgs* P, size_t* smem)
         return false;
     P->bands = (unsigned)(g.bands * g.C);
     const int rows = g.nw * g.w;
-    long long nb = kBandThreads / rows;
+    // two window rows a thread, one where that would leave SMs without blocks
+    long long nb = kBandThreads * kBandRows / rows;
+    if (P->bands < nb * 4 * num_sms)
+        nb = kBandThreads / rows;
     nb = nb < 1 ? 1 : nb > kBandElems / bn ? kBandElems / bn : nb;
     P->nb = (int)nb;
     P->div_row = ceil_recip(rows);
     P->div_nw = ceil_recip(g.nw);
-    *smem = (nb * bn * sz + 31) / 16 * 16 + (nb * bn + 15) / 16 * 16 + (size_t)nb * (g.nw + 1) * 4;
+    *smem = 16 + (nb * bn * sz + 31) / 16 * 16 + (nb * bn + 15) / 16 * 16 + (size_t)nb * (g.nw + 1) * 4;
     return *smem <= 48 * 1024;
 }
 
-// KernelT<T, WS, EVEN>::run for the window size.
-template <template <typename, int, bool> class KernelT, typename T, typename... Args>
-cudaError_t band_launch(const BandArgs& P, size_t smem, const Launch& L, Args... args)
+template <template <typename, int> class KernelT, typename T, int WS>
+auto pick_kernel(int w)
 {
-    auto kernel = P.w == 14 ? KernelT<T, 14, true>::get()
-                  : P.w == 7 ? KernelT<T, 7, false>::get()
-                  : P.w % 2 == 0 ? KernelT<T, 0, true>::get()
-                                 : KernelT<T, 0, false>::get();
-    const dim3 grid((unsigned)((P.bands + P.nb - 1) / P.nb)), block(kBandThreads);
-    return launch_pdl(kernel, grid, block, smem, L.stream, args..., P);
+    if constexpr (WS < 2)
+        return KernelT<T, 0>::get();
+    else
+        return w == WS ? KernelT<T, WS>::get() : pick_kernel<KernelT, T, WS - 1>(w);
 }
 
-template <typename T, int WS, bool EVEN>
+template <template <typename, int> class KernelT, typename T, typename... Args>
+cudaError_t band_launch(const BandArgs& P, size_t smem, const Launch& L, Args... args)
+{
+    const dim3 grid((P.bands + P.nb - 1) / P.nb), block(kBandThreads);
+    // the compiled sizes hold a block's window rows in registers
+    const bool fits = P.nb * P.nw * P.w <= kBandThreads * kBandRows;
+    return launch_pdl(fits ? pick_kernel<KernelT, T, 16>(P.w) : KernelT<T, 0>::get(), grid, block, smem, L.stream, args..., P);
+}
+
+template <typename T, int WS>
 struct StoreKernel {
-    static constexpr auto get() { return &ckpt_store_bands_kernel<T, WS, EVEN>; }
+    static constexpr auto get() { return &ckpt_store_bands_kernel<T, WS>; }
 };
 
-template <typename T, int WS, bool EVEN>
+template <typename T, int WS>
 struct RestoreKernel {
-    static constexpr auto get() { return &ckpt_restore_bands_kernel<T, WS, EVEN>; }
+    static constexpr auto get() { return &ckpt_restore_bands_kernel<T, WS>; }
 };
 
 unsigned warp_grid(long long warps, const Launch& L)
@@ -395,7 +504,7 @@ cudaError_t checkpoint_launch(const Geom& g, bool is_bf16, const void* x, uint8_
     cudaError_t e;
     const long long nwin = g.bands * g.nw;
     const dim3 grid(warp_grid(nwin * g.C, L)), block(128);
-    if (band_args(g, is_bf16 ? 2 : 4, &P, &smem))
+    if (band_args(g, is_bf16 ? 2 : 4, L.num_sms, &P, &smem))
         e = is_bf16 ? band_launch<StoreKernel, __nv_bfloat16>(
                           P, smem, L, static_cast<const __nv_bfloat16*>(x), codes, exps)
                     : band_launch<StoreKernel, float>(P, smem, L, static_cast<const float*>(x), codes,
@@ -421,7 +530,7 @@ cudaError_t checkpoint_restore_launch(const Geom& g, bool is_bf16, const uint8_t
     cudaError_t e;
     const long long nwin = g.bands * g.nw;
     const dim3 grid(warp_grid(nwin * g.C, L)), block(128);
-    if (band_args(g, is_bf16 ? 2 : 4, &P, &smem))
+    if (band_args(g, is_bf16 ? 2 : 4, L.num_sms, &P, &smem))
         e = is_bf16 ? band_launch<RestoreKernel, __nv_bfloat16>(P, smem, L, codes, exps,
                                                                 static_cast<__nv_bfloat16*>(x))
                     : band_launch<RestoreKernel, float>(P, smem, L, codes, exps,
