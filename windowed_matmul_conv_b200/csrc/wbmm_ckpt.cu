@@ -107,6 +107,8 @@ struct BandArgs {
     unsigned bands;         // of all planes
     unsigned div_row;       // ceil(2^32 / (nw w)) and / nw, 0 for a divisor of 1
     unsigned div_nw;
+    int unit, units;        // bytes a copy of codes moves, copies a band
+    unsigned div_units;
 };
 
 // n / d for n d < 2^32, m = ceil(2^32 / d).
@@ -276,20 +278,16 @@ __global__ void __launch_bounds__(kBandThreads)
     grid_dep_launch();
     const T* src = x + (long long)f0 * bn;
     const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
-    {
-        const uint8_t* at = reinterpret_cast<const uint8_t*>(src);
-        const uint8_t* end = at + (long long)nb * bn * (int)sizeof(T);
-        for (const uint8_t* p = at - off + 16 * tid; p < end; p += 16 * kBandThreads) {
-            const uint32_t to = smem_u32(img + (p - (at - off)));
-            if (p >= at && p + 16 <= end) {
-                cp_async_16z(to, p, 16u);
-            } else {
-                // the block's first and last partial 16 bytes, by elements
-                for (int q = 0; q < 16; q += (int)sizeof(T))
-                    if (p + q >= at && p + q < end)
-                        *reinterpret_cast<T*>(img + (p + q - (at - off))) =
-                            *reinterpret_cast<const T*>(p + q);
-            }
+    const int bytes = nb * bn * (int)sizeof(T);
+    for (int lo = 16 * tid - off; lo < bytes; lo += 16 * kBandThreads) {
+        const uint8_t* from = reinterpret_cast<const uint8_t*>(src) + lo;
+        if (lo >= 0 && lo + 16 <= bytes) {
+            cp_async_16z(smem_u32(img + off + lo), from, 16u);
+        } else {
+            // the first and last partial 16 bytes, by elements
+            for (int q = 0; q < 16; q += (int)sizeof(T))
+                if (lo + q >= 0 && lo + q < bytes)
+                    *reinterpret_cast<T*>(img + off + lo + q) = *reinterpret_cast<const T*>(from + q);
         }
     }
     cp_async_wait_all();
@@ -345,23 +343,21 @@ __global__ void __launch_bounds__(kBandThreads)
         }
     }
     __syncthreads();
-    for (int band = tid / 32; band < nb; band += kBandThreads / 32) {
-        const int lane = tid & 31;
-        const unsigned n = place[band];
-        uint8_t* out = codes + (long long)n * bn;
-        const uint8_t* in = cds + band * bn;
-        if (bn % 8 == 0) {
-            for (int k = lane; k < bn / 8; k += 32)
-                reinterpret_cast<uint2*>(out)[k] = reinterpret_cast<const uint2*>(in)[k];
-        } else if (bn % 4 == 0) {
-            for (int k = lane; k < bn / 4; k += 32)
-                reinterpret_cast<uint32_t*>(out)[k] = reinterpret_cast<const uint32_t*>(in)[k];
-        } else {
-            for (int k = lane; k < bn; k += 32)
-                out[k] = in[k];
-        }
-        for (int k = lane; k < P.nw; k += 32)
-            exps[(long long)n * P.nw + k] = (uint8_t)group_exp(top[band * P.nw + k]);
+    for (int k = tid; k < nb * P.units; k += kBandThreads) {
+        const int band = fast_div(k, P.div_units);
+        const int at = (k - band * P.units) * P.unit;
+        uint8_t* out = codes + (long long)place[band] * bn + at;
+        const uint8_t* in = cds + band * bn + at;
+        if (P.unit == 8)
+            *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(in);
+        else if (P.unit == 4)
+            *reinterpret_cast<uint32_t*>(out) = *reinterpret_cast<const uint32_t*>(in);
+        else
+            *out = *in;
+    }
+    for (int k = tid; k < windows; k += kBandThreads) {
+        const int band = fast_div(k, P.div_nw);
+        exps[(long long)place[band] * P.nw + (k - band * P.nw)] = (uint8_t)group_exp(top[k]);
     }
 }
 
@@ -385,23 +381,21 @@ __global__ void __launch_bounds__(kBandThreads)
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    for (int band = tid / 32; band < nb; band += kBandThreads / 32) {
-        const int lane = tid & 31;
-        const unsigned n = place[band];
-        const uint8_t* in = codes + (long long)n * bn;
-        uint8_t* to = cds + band * bn;
-        if (bn % 8 == 0) {
-            for (int k = lane; k < bn / 8; k += 32)
-                cp_async_8(smem_u32(to + 8 * k), in + 8 * k);
-        } else if (bn % 4 == 0) {
-            for (int k = lane; k < bn / 4; k += 32)
-                cp_async_4(smem_u32(to + 4 * k), in + 4 * k);
-        } else {
-            for (int k = lane; k < bn; k += 32)
-                to[k] = in[k];
-        }
-        for (int k = lane; k < P.nw; k += 32)
-            step[band * P.nw + k] = step_of(exps[(long long)n * P.nw + k]);
+    for (int k = tid; k < nb * P.units; k += kBandThreads) {
+        const int band = fast_div(k, P.div_units);
+        const int at = (k - band * P.units) * P.unit;
+        const uint8_t* in = codes + (long long)place[band] * bn + at;
+        uint8_t* to = cds + band * bn + at;
+        if (P.unit == 8)
+            cp_async_8(smem_u32(to), in);
+        else if (P.unit == 4)
+            cp_async_4(smem_u32(to), in);
+        else
+            *to = *in;
+    }
+    for (int k = tid; k < windows; k += kBandThreads) {
+        const int band = fast_div(k, P.div_nw);
+        step[k] = step_of(exps[(long long)place[band] * P.nw + (k - band * P.nw)]);
     }
     cp_async_wait_all();
     __syncthreads();
@@ -421,16 +415,16 @@ __global__ void __launch_bounds__(kBandThreads)
         }
     }
     __syncthreads();
-    uint8_t* at = reinterpret_cast<uint8_t*>(dst);
-    uint8_t* end = at + (long long)nb * bn * (int)sizeof(T);
-    for (uint8_t* p = at - off + 16 * tid; p < end; p += 16 * kBandThreads) {
-        const uint8_t* from = img + (p - (at - off));
-        if (p >= at && p + 16 <= end) {
-            *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(from);
+    const int bytes = nb * bn * (int)sizeof(T);
+    for (int lo = 16 * tid - off; lo < bytes; lo += 16 * kBandThreads) {
+        uint8_t* to = reinterpret_cast<uint8_t*>(dst) + lo;
+        const uint8_t* from = img + off + lo;
+        if (lo >= 0 && lo + 16 <= bytes) {
+            *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
         } else {
             for (int q = 0; q < 16; q += (int)sizeof(T))
-                if (p + q >= at && p + q < end)
-                    *reinterpret_cast<T*>(p + q) = *reinterpret_cast<const T*>(from + q);
+                if (lo + q >= 0 && lo + q < bytes)
+                    *reinterpret_cast<T*>(to + q) = *reinterpret_cast<const T*>(from + q);
         }
     }
 }
@@ -456,6 +450,9 @@ bool band_args(const Geom& g, size_t sz, int num_sms, BandArgs* P, size_t* smem)
     P->nb = (int)nb;
     P->div_row = ceil_recip(rows);
     P->div_nw = ceil_recip(g.nw);
+    P->unit = bn % 8 == 0 ? 8 : bn % 4 == 0 ? 4 : 1;
+    P->units = (int)bn / P->unit;
+    P->div_units = ceil_recip(P->units);
     *smem = 16 + (nb * bn * sz + 31) / 16 * 16 + (nb * bn + 15) / 16 * 16 + (size_t)nb * (g.nw + 1) * 4;
     return *smem <= 48 * 1024;
 }
