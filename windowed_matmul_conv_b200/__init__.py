@@ -458,8 +458,12 @@ def backward_checkpoint(codes, exps, T, dY, w, need_dx=True, need_dt=True, strea
     ws = None
     if need_dt:
         nbytes = wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dY.dtype)
-        ws = torch.empty(max(1, (nbytes + 3) // 4), dtype=torch.float32, device=dY.device)
-        ws[:WBMM_DT_COUNTER_WORDS].zero_()      # the arrival counters start at zero
+        # the arrival counters start at zero; a restored map behind them need not
+        if nbytes == wbmm_backward_workspace_bytes(B, C, H, W, w, dY.dtype):
+            ws = torch.zeros(nbytes // 4, dtype=torch.float32, device=dY.device)
+        else:
+            ws = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=dY.device)
+            ws[:WBMM_DT_COUNTER_WORDS].zero_()
     wbmm_backward_checkpoint(codes, exps, T, dY, dX, dT, ws, w, stream)
     return dX, dT
 

@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "ptx_sm100.cuh"
 
 namespace wbmm {
@@ -81,14 +82,20 @@ struct TransformCfg {
 };
 
 template <int WS>
+struct TransformRows {
+    static constexpr int NROW = 32 / TransformCfg<WS>::NWIN;
+    static constexpr int RQ = (WS + NROW - 1) / NROW;   // window rows a lane
+};
+
+template <int WS, int Q0 = 0, int Q1 = TransformRows<WS>::RQ>
 __device__ __forceinline__ void transform_group(const uint16_t* raw, uint8_t* dst, uint32_t sbo,
                                                 int gi, int nwin, int nend, const int* woff,
                                                 int W, int lane)
 {
     using P = PadCfg<WS>;
     constexpr int NWIN = TransformCfg<WS>::NWIN;
-    constexpr int NROW = 32 / NWIN;
-    constexpr int RQ = (WS + NROW - 1) / NROW;
+    constexpr int NROW = TransformRows<WS>::NROW;
+    constexpr int RQ = Q1 - Q0;
     const int nl = lane % NWIN, rs = lane / NWIN;
     const int n = gi * NWIN + nl;
     if (n >= nend)
@@ -97,7 +104,7 @@ __device__ __forceinline__ void transform_group(const uint16_t* raw, uint8_t* ds
     uint32_t wv[RQ][P::RP / 2];
 #pragma unroll
     for (int q = 0; q < RQ; ++q) {
-        const int r = q * NROW + rs;
+        const int r = (Q0 + q) * NROW + rs;
         const uint16_t* src = base + r * W;
         if (n >= nwin || r >= WS) {
 #pragma unroll
@@ -119,13 +126,69 @@ __device__ __forceinline__ void transform_group(const uint16_t* raw, uint8_t* ds
     uint8_t* d0 = dst + (n >> 3) * sbo + (n & 7) * 16;
 #pragma unroll
     for (int q = 0; q < RQ; ++q) {
-        const int r = q * NROW + rs;
+        const int r = (Q0 + q) * NROW + rs;
         if (r >= WS)
             continue;
 #pragma unroll
         for (int c = 0; c < P::RP / 8; ++c)
             *reinterpret_cast<uint4*>(d0 + (r * P::RP / 8 + c) * 128) =
                 make_uint4(wv[q][4 * c], wv[q][4 * c + 1], wv[q][4 * c + 2], wv[q][4 * c + 3]);
+    }
+}
+
+// transform_group for a group of windows held as 8-bit codes, window n's at
+// byte n * WS * WS of `codes` (WS even: at even bytes) with step[n], window
+// rows q0 <= q < q1 of the lane's RQ.  The restored values are exact in bf16.
+template <int WS, int Q0, int Q1>
+__device__ __forceinline__ void transform_group_codes(const uint8_t* codes, const float* step,
+                                                      uint8_t* dst, uint32_t sbo, int gi, int nwin,
+                                                      int nend, int lane)
+{
+    using P = PadCfg<WS>;
+    constexpr int NWIN = TransformCfg<WS>::NWIN;
+    constexpr int NROW = 32 / NWIN;
+    const int nl = lane % NWIN, rs = lane / NWIN;
+    const int n = gi * NWIN + nl;
+    if (n >= nend)
+        return;
+    const bool real = n < nwin;
+    const uint8_t* base = codes + (real ? n : 0) * P::D;
+    const float st = step[real ? n : 0];
+    uint8_t* d0 = dst + (n >> 3) * sbo + (n & 7) * 16;
+#pragma unroll
+    for (int q = Q0; q < Q1; ++q) {
+        const int r = q * NROW + rs;
+        if (r >= WS)
+            continue;
+        const uint8_t* src = base + r * WS;
+        uint32_t w[P::RP / 2];
+#pragma unroll
+        for (int m = 0; m < P::RP / 2; ++m) {
+            w[m] = 0u;
+            if (2 * m >= WS)
+                continue;
+            uint32_t a, b;
+            if constexpr (WS % 2 == 0) {
+                const uint32_t u = reinterpret_cast<const uint16_t*>(src)[m];
+                a = __byte_perm(u, 0x4b000000u, 0x7440);
+                b = __byte_perm(u, 0x4b000000u, 0x7441);
+            } else {
+                a = 0x4b000000u | src[2 * m];
+                b = 2 * m + 1 < WS ? 0x4b000000u | src[2 * m + 1] : 0x4b000080u;
+            }
+            // 2^23 + code, less 2^23 + 128, times the step; upper halves
+            const F2 v = mul2(add2({__uint_as_float(a), __uint_as_float(b)},
+                                   {-8388736.0f, -8388736.0f}), {st, st});
+            w[m] = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+            if (2 * m + 1 >= WS)
+                w[m] &= 0xffffu;        // padding stays zero under a NaN step
+            if (!real)
+                w[m] = 0u;
+        }
+#pragma unroll
+        for (int c = 0; c < P::RP / 8; ++c)
+            *reinterpret_cast<uint4*>(d0 + (r * P::RP / 8 + c) * 128) =
+                make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     }
 }
 
@@ -159,6 +222,43 @@ __device__ __forceinline__ void transform_rows_pair(const uint16_t* raw0, uint8_
         const bool second = it >= groups;
         transform_group<WS>(second ? raw1 : raw0, second ? dst1 : dst0, sbo,
                             second ? it - groups : it, nwin, nend, woff, W, lane);
+    }
+}
+
+// transform_rows_pair with the second tile's windows held as 8-bit codes.
+// Where a tile has as many groups as half the warps (16-window groups), a warp
+// takes part of the rows of one group of each tensor, since codes cost more
+// than a copy of bf16 words.
+template <int WS>
+__device__ __forceinline__ void transform_rows_codes(const uint16_t* raw0, uint8_t* dst0,
+                                                     const uint8_t* codes, const float* step,
+                                                     uint8_t* dst1, uint32_t sbo, int nwin,
+                                                     int nzero, const int* woff, int W, int tid,
+                                                     int nthreads)
+{
+    constexpr int NWIN = TransformCfg<WS>::NWIN;
+    constexpr int RQ = TransformRows<WS>::RQ, HALF = (RQ + 1) / 2;
+    const int lane = tid & 31, wid = tid >> 5, nwarps = nthreads >> 5;
+    const int nend = nzero > nwin ? nzero : nwin;
+    const int groups = (nend + NWIN - 1) / NWIN;
+    if constexpr (NWIN == 16) {
+        for (int it = wid; it < 2 * groups; it += nwarps) {
+            const int gi = it >> 1;
+            if (it & 1) {
+                transform_group<WS, 0, HALF>(raw0, dst0, sbo, gi, nwin, nend, woff, W, lane);
+                transform_group_codes<WS, HALF, RQ>(codes, step, dst1, sbo, gi, nwin, nend, lane);
+            } else {
+                transform_group<WS, HALF, RQ>(raw0, dst0, sbo, gi, nwin, nend, woff, W, lane);
+                transform_group_codes<WS, 0, HALF>(codes, step, dst1, sbo, gi, nwin, nend, lane);
+            }
+        }
+    } else {
+        for (int it = wid; it < 2 * groups; it += nwarps) {
+            if (it >= groups)
+                transform_group_codes<WS, 0, RQ>(codes, step, dst1, sbo, it - groups, nwin, nend, lane);
+            else
+                transform_group<WS>(raw0, dst0, sbo, it, nwin, nend, woff, W, lane);
+        }
     }
 }
 

@@ -144,7 +144,7 @@ size_t code_bytes(const Geom& g) { return (size_t)g.B * g.C * g.H * g.W; }
 
 size_t exp_bytes(const Geom& g) { return (size_t)g.C * (size_t)g.bands * g.nw; }
 
-// Where wbmm_backward_checkpoint keeps the restored map in its workspace.
+// Where wbmm_backward_checkpoint keeps a restored map in its workspace.
 size_t ckpt_map_offset(const Geom& g, wbmm_dtype dt)
 {
     return ((size_t)dt_workspace_floats(g, dt) * 4 + 15) / 16 * 16;
@@ -187,9 +187,17 @@ bool clash(const Span* in, int nin, const Span* out, int nout, const void* carry
     return false;
 }
 
-// The launches of a backward call whose arguments have been checked; x is
-// used by the table gradient only.
-wbmm_status backward_run(const Geom& g, const void* x, const void* T, const void* dY, void* dX,
+// The table gradient reads an 8-bit checkpoint as it is; otherwise the map is
+// restored into the workspace.
+bool reads_codes(const Geom& g, wbmm_dtype dt)
+{
+    return dt == WBMM_BF16 && tc_dt_codes_supported(g);
+}
+
+// The launches of a backward call whose arguments have been checked; x, or
+// where it is null codes and exps, is used by the table gradient only.
+wbmm_status backward_run(const Geom& g, const void* x, const unsigned char* codes,
+                         const unsigned char* exps, const void* T, const void* dY, void* dX,
                          float* dT, void* workspace, wbmm_dtype dt, const Launch& L)
 {
     wbmm_status st = WBMM_OK;
@@ -230,7 +238,8 @@ wbmm_status backward_run(const Geom& g, const void* x, const void* T, const void
             // dX, when requested, was the launch just before this one (every
             // library kernel signals its dependents only after its own wait)
             const bool after_dx = dX != nullptr;
-            st = from_cuda(tc_dt_launch(g, x, dY, part, dT, after_dx, Lt));
+            st = from_cuda(x ? tc_dt_launch(g, x, dY, part, dT, after_dx, Lt)
+                             : tc_dt_codes_launch(g, codes, exps, dY, part, dT, after_dx, Lt));
         } else {
             float* chunks = part + WBMM_DT_COUNTER_WORDS;
             st = from_cuda(simt_dt_launch(g, dt == WBMM_BF16, x, dY, chunks, L));
@@ -420,7 +429,7 @@ wbmm_status wbmm_backward(const void* x, const void* T, const void* dY, void* dX
     Launch L;
     if ((st = make_launch(stream, &L)) != WBMM_OK)
         return st;
-    return backward_run(g, x, T, dY, dX, dT, workspace, dt, L);
+    return backward_run(g, x, nullptr, nullptr, T, dY, dX, dT, workspace, dt, L);
 }
 
 wbmm_status wbmm_cache_matrices(const void* T, void* M, int C, int w, wbmm_dtype dt,
@@ -579,7 +588,8 @@ size_t wbmm_backward_checkpoint_workspace_bytes(int B, int C, int H, int W, int 
     if (!dtype_ok(dt) || check_map(B, C, H, W, w) != WBMM_OK)
         return 0;
     const Geom g = make_geom(B, C, H, W, w);
-    return ckpt_map_offset(g, dt) + map_bytes(g, dt);
+    return reads_codes(g, dt) ? (size_t)dt_workspace_floats(g, dt) * 4
+                              : ckpt_map_offset(g, dt) + map_bytes(g, dt);
 }
 
 wbmm_status wbmm_backward_checkpoint(const unsigned char* codes, const unsigned char* exps,
@@ -622,13 +632,13 @@ wbmm_status wbmm_backward_checkpoint(const unsigned char* codes, const unsigned 
     if ((st = make_launch(stream, &L)) != WBMM_OK)
         return st;
     void* x = nullptr;
-    if (dT) {
+    if (dT && !reads_codes(g, dt)) {
         x = static_cast<char*>(workspace) + ckpt_map_offset(g, dt);
         st = from_cuda(checkpoint_restore_launch(g, dt == WBMM_BF16, codes, exps, x, L));
         if (st != WBMM_OK)
             return st;
     }
-    return backward_run(g, x, T, dY, dX, dT, workspace, dt, L);
+    return backward_run(g, x, codes, exps, T, dY, dX, dT, workspace, dt, L);
 }
 
 size_t wbmm_scan_states_bytes(int B, int C, int L)

@@ -251,8 +251,8 @@ __device__ __forceinline__ void restore_row(T* e, const uint8_t* c, float st)
     }
 }
 
-// WS: the window size, 2 to 16 as the tensor-core kernels compile for, or 0
-// for any other (w as given).
+// WS: the window size, 2 to 16 or 28 as the tensor-core kernels compile for,
+// or 0 for any other (w as given).
 template <typename T, int WS>
 __global__ void __launch_bounds__(kBandThreads)
     ckpt_store_bands_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes,
@@ -472,7 +472,10 @@ cudaError_t band_launch(const BandArgs& P, size_t smem, const Launch& L, Args...
     const dim3 grid((P.bands + P.nb - 1) / P.nb), block(kBandThreads);
     // the compiled sizes hold a block's window rows in registers
     const bool fits = P.nb * P.nw * P.w <= kBandThreads * kBandRows;
-    return launch_pdl(fits ? pick_kernel<KernelT, T, 16>(P.w) : KernelT<T, 0>::get(), grid, block, smem, L.stream, args..., P);
+    return launch_pdl(!fits        ? KernelT<T, 0>::get()
+                      : P.w == 28 ? KernelT<T, 28>::get()
+                                  : pick_kernel<KernelT, T, 16>(P.w),
+                      grid, block, smem, L.stream, args..., P);
 }
 
 template <typename T, int WS>

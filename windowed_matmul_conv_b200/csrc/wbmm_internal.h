@@ -93,6 +93,13 @@ long long tc_dt_workspace_floats(const Geom& g);
 cudaError_t tc_dt_launch(const Geom& g, const void* x, const void* dy, float* workspace, float* dT,
                          bool after_dx, const Launch& L);
 
+// The same with x as an 8-bit checkpoint (a channel's codes a multiple of 16
+// bytes); equal, bit for bit, to tc_dt_launch on the restored map.
+bool tc_dt_codes_supported(const Geom& g);
+cudaError_t tc_dt_codes_launch(const Geom& g, const uint8_t* codes, const uint8_t* exps,
+                               const void* dy, float* workspace, float* dT, bool after_dx,
+                               const Launch& L);
+
 // CUDA-core kernels.  is_bf16 selects the element type of every map/table.
 int simt_dt_chunks(const Geom& g);
 cudaError_t simt_fwd_launch(const Geom& g, AMode mode, bool is_bf16, const void* x,

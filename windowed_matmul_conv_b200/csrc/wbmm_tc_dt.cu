@@ -43,6 +43,7 @@
 // partial table.
 #include <cuda_bf16.h>
 
+#include "ckpt_common.cuh"
 #include "ptx_sm100.cuh"
 #include "wbmm.h"
 #include "tc_common.cuh"
@@ -93,6 +94,10 @@ struct DtCfg : PadCfg<WS> {
     static constexpr uint32_t STAGE_BYTES = 2 * TILE_BYTES;     // dY tile, then x tile
     static constexpr uint32_t RAW_HALF = (uint32_t)((NT * P::D * 2 + 127) / 128 * 128);
     static constexpr uint32_t RAW_BYTES = 2 * RAW_HALF;
+    // a slot whose x half holds 8-bit codes (from a 16-byte boundary on, whole
+    // 16-byte pieces) and the windows' steps
+    static constexpr uint32_t CODE_HALF = (uint32_t)((NT * P::D + 32 + 127) / 128 * 128);
+    static constexpr uint32_t RAW_CODES = RAW_HALF + CODE_HALF + (uint32_t)(NT * 4);
     // kind::f16, bf16 A and B, both MN-major (positions contiguous), fp32 D
     static constexpr uint32_t IDESC = idesc_bf16(128, NPOS) | (1u << 15) | (1u << 16);
     static_assert(NPOS <= 256 && MT <= 2, "G must fit in TMEM");
@@ -103,6 +108,8 @@ struct TcDtParams {
     TmapBytes map_dy;
     const uint16_t* x;
     const uint16_t* dy;
+    const uint8_t* codes;   // x as 8-bit codes [C][windows][w*w] (CODES)
+    const uint8_t* exps;    // and exponent bytes [C][windows]
     float* partials;        // [C + grid - 1][tsz], segment (c, k) at c + k
     unsigned int* counters; // [C] segments of channel c written so far (zero between launches)
     float* dT;              // [C][tsz]
@@ -183,10 +190,15 @@ struct DtWalker {
     __device__ __forceinline__ void next(const TcDtParams&) { ++t; }
 };
 
-template <int WS>
+// CODES: x comes as an 8-bit checkpoint.  A tile's windows are one run of
+// codes (one bulk copy); the producer warp keeps the exponent bytes of the
+// next tile in registers and leaves a tile's steps in its slot; the transform
+// restores the values, which bf16 holds exactly, on their way to the operand.
+template <int WS, bool CODES>
 __global__ void __launch_bounds__(kDtThreads, 1) wbmm_tc_dt_kernel(const __grid_constant__ TcDtParams P)
 {
     using F = DtCfg<WS>;
+    constexpr uint32_t RAW = CODES ? F::RAW_CODES : F::RAW_BYTES;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* raw_base = smem + P.off_raw;
@@ -242,7 +254,20 @@ __global__ void __launch_bounds__(kDtThreads, 1) wbmm_tc_dt_kernel(const __grid_
         // Lane 0 arms the slot's barrier; the lanes issue one run each.
         int issued = 0, seq = 0;
         DtWalker it;
-        for (it.start(P); it.valid(P); it.next(P), ++seq) {
+        // CODES: the exponent bytes of windows lane, lane + 32 of a tile
+        uint32_t ex[2] = {0u, 0u};
+        const long long chan = (long long)P.bands * P.nw;   // windows a channel
+        auto load_exps = [&](const DtTile& t) {
+            const uint8_t* e = P.exps + t.bt.c * chan + (long long)t.bt.band0 * P.nw;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (lane + 32 * k < t.bt.nb * P.nw)
+                    ex[k] = __ldg(e + lane + 32 * k);
+        };
+        it.start(P);
+        if (CODES && it.valid(P))
+            load_exps(it.get(P));
+        for (; it.valid(P); it.next(P), ++seq) {
             const int s = seq % P.R;
             bool ok = !*abort;
             if (seq >= P.R)
@@ -251,10 +276,49 @@ __global__ void __launch_bounds__(kDtThreads, 1) wbmm_tc_dt_kernel(const __grid_
             if (!__all_sync(0xffffffffu, ok))
                 break;
             const DtTile t = it.get(P);
-            uint8_t* slot = raw_base + (size_t)s * F::RAW_BYTES;
+            uint8_t* slot = raw_base + (size_t)s * RAW;
+            if constexpr (CODES) {
+                float* step = reinterpret_cast<float*>(slot + F::RAW_HALF + F::CODE_HALF);
+#pragma unroll
+                for (int k = 0; k < (F::NT + 31) / 32; ++k)
+                    step[lane + 32 * k] = step_of(ex[k]);
+                DtWalker ahead = it;
+                ahead.next(P);
+                if (ahead.valid(P))
+                    load_exps(ahead.get(P));
+                __syncwarp();   // lane 0's arrival below covers the steps
+            }
             if (seq == P.skip_seq && blockIdx.x == 0) {
                 // test only: the slot is never armed, so the transform's
                 // bounded wait for it runs out
+                issued = seq + 1;
+                continue;
+            }
+            if constexpr (CODES) {
+                // the 16-byte pieces that hold the tile's codes; a channel's
+                // codes start and end on 16-byte boundaries
+                const long long first =
+                    (t.bt.c * chan + (long long)t.bt.band0 * P.nw) * F::D;
+                const uint32_t lead = (uint32_t)(first & 15);
+                const uint32_t bytes = (lead + (uint32_t)(t.bt.nb * P.nw * F::D) + 15u) & ~15u;
+                const uint32_t dy_bytes = P.use_tmap ? (uint32_t)P.kimg * WS * P.W * P.nh * 2
+                                                     : (uint32_t)t.bt.nb * WS * P.W * 2;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&S.raw_full[s], dy_bytes + bytes);
+                    bulk_g2s(slot + F::RAW_HALF, P.codes + (first - lead), bytes, &S.raw_full[s]);
+                    if (P.use_tmap)
+                        tma_load_4d(slot, &P.map_dy, 0, 0, t.bt.c, t.bt.band0 / P.nh, &S.raw_full[s]);
+                }
+                __syncwarp();
+                if (!P.use_tmap) {
+                    const BandRuns runs = band_runs(t.bt, P.nh);
+                    for (int l = lane; l < runs.count; l += 32) {
+                        long long goff;
+                        uint32_t soff, nbytes;
+                        band_run(t.bt, runs, l, WS, P.W, P.H, P.C, P.nh, goff, soff, nbytes);
+                        bulk_g2s(slot + soff, P.dy + goff, nbytes, &S.raw_full[s]);
+                    }
+                }
                 issued = seq + 1;
                 continue;
             }
@@ -355,14 +419,25 @@ __global__ void __launch_bounds__(kDtThreads, 1) wbmm_tc_dt_kernel(const __grid_
                                      P.status);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
-                const uint16_t* raw =
-                    reinterpret_cast<const uint16_t*>(raw_base + (size_t)s * F::RAW_BYTES);
+                const uint8_t* slot = raw_base + (size_t)s * RAW;
+                const uint16_t* raw = reinterpret_cast<const uint16_t*>(slot);
                 uint8_t* stage = st_base + (size_t)bs * F::STAGE_BYTES;
                 const int nwin = t.bt.nb * P.nw;
                 const int nzero = (nwin + 15) & ~15;    // last MMA K step reads up to here
-                transform_rows_pair<WS>(raw, stage, raw + F::RAW_HALF / 2, stage + F::TILE_BYTES,
-                                        F::SBO_T, nwin, nzero, woff, P.W, tt,
-                                        kDtXformWarps * 32);
+                if constexpr (CODES) {
+                    // a channel's codes are whole 16-byte pieces, so the lead
+                    // depends on the tile's place within its channel only
+                    const int lead = (int)(((long long)t.bt.band0 * P.nw * F::D) & 15);
+                    transform_rows_codes<WS>(
+                        raw, stage, slot + F::RAW_HALF + lead,
+                        reinterpret_cast<const float*>(slot + F::RAW_HALF + F::CODE_HALF),
+                        stage + F::TILE_BYTES, F::SBO_T, nwin, nzero, woff, P.W, tt,
+                        kDtXformWarps * 32);
+                } else {
+                    transform_rows_pair<WS>(raw, stage, raw + F::RAW_HALF / 2,
+                                            stage + F::TILE_BYTES, F::SBO_T, nwin, nzero, woff,
+                                            P.W, tt, kDtXformWarps * 32);
+                }
                 fence_proxy_async_smem();
             }
             __syncwarp();
@@ -560,10 +635,11 @@ struct DtLayout {
 
 // Operand stages | staging array | window offsets | barriers | raw ring,
 // as many raw slots as fit (at most kDtRingMax).
-template <int WS>
+template <int WS, bool CODES>
 DtLayout dt_layout()
 {
     using F = DtCfg<WS>;
+    constexpr uint32_t RAW = CODES ? F::RAW_CODES : F::RAW_BYTES;
     DtLayout L;
     uint32_t off = 0;
     L.off_stage = off;
@@ -576,12 +652,12 @@ DtLayout dt_layout()
     off = L.off_bar + sizeof(DtBars);
     L.off_raw = align_up(off, 128);
     const uint32_t avail = kSmemMax - 1024 > L.off_raw ? kSmemMax - 1024 - L.off_raw : 0;
-    int R = (int)(avail / F::RAW_BYTES);
+    int R = (int)(avail / RAW);
     L.R = R < kDtRingMax ? R : kDtRingMax;
     const int cap = debug_ring_cap();
     if (cap >= 2 && L.R > cap)
         L.R = cap;
-    off = L.off_raw + (uint32_t)L.R * F::RAW_BYTES;
+    off = L.off_raw + (uint32_t)L.R * RAW;
     L.total = align_up(off, 1024);
     // at least half the SM's shared memory: one CTA (and one 512-column TMEM
     // allocation) per SM
@@ -608,19 +684,19 @@ long long tc_dt_partials_impl(const Geom& g)
     return g.C + (tiles < kDtMaxGrid ? tiles : kDtMaxGrid) - 1;
 }
 
-template <int WS>
-cudaError_t dt_launch_ws(const Geom& g, const void* x, const void* dy, float* workspace,
-                         float* dT, bool after_dx, const Launch& L)
+template <int WS, bool CODES>
+cudaError_t dt_launch_ws(const Geom& g, const void* x, const uint8_t* exps, const void* dy,
+                         float* workspace, float* dT, bool after_dx, const Launch& L)
 {
     using F = DtCfg<WS>;
-    const DtLayout lay = dt_layout<WS>();
+    const DtLayout lay = dt_layout<WS, CODES>();
     if (lay.total > kSmemMax || lay.R < 2)
         return cudaErrorInvalidConfiguration;
     static unsigned long long configured = 0;
     int dev = 0;
     cudaGetDevice(&dev);
     if (!(configured & (1ull << (dev & 63)))) {
-        cudaError_t e = cudaFuncSetAttribute(wbmm_tc_dt_kernel<WS>,
+        cudaError_t e = cudaFuncSetAttribute(wbmm_tc_dt_kernel<WS, CODES>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kSmemMax);
         if (e != cudaSuccess)
@@ -628,7 +704,9 @@ cudaError_t dt_launch_ws(const Geom& g, const void* x, const void* dy, float* wo
         configured |= 1ull << (dev & 63);
     }
     TcDtParams P;
-    P.x = static_cast<const uint16_t*>(x);
+    P.x = CODES ? nullptr : static_cast<const uint16_t*>(x);
+    P.codes = CODES ? static_cast<const uint8_t*>(x) : nullptr;
+    P.exps = exps;
     P.dy = static_cast<const uint16_t*>(dy);
     P.counters = reinterpret_cast<unsigned int*>(workspace);
     P.partials = workspace + WBMM_DT_COUNTER_WORDS;
@@ -662,7 +740,7 @@ cudaError_t dt_launch_ws(const Geom& g, const void* x, const void* dy, float* wo
     P.kimg = 0;
     if (P.bpt % g.nh == 0) {
         const int k = P.bpt / g.nh;
-        if (encode_plane_map(&P.map_x, x, g, k) && encode_plane_map(&P.map_dy, dy, g, k)) {
+        if ((CODES || encode_plane_map(&P.map_x, x, g, k)) && encode_plane_map(&P.map_dy, dy, g, k)) {
             P.use_tmap = 1;
             P.kimg = k;
         }
@@ -673,7 +751,7 @@ cudaError_t dt_launch_ws(const Geom& g, const void* x, const void* dy, float* wo
     P.budget = L.budget;
     P.status = L.status;
     P.skip_seq = debug_take_skip(1);
-    cudaError_t e = launch_pdl(wbmm_tc_dt_kernel<WS>, dim3(grid), dim3(kDtThreads), lay.total,
+    cudaError_t e = launch_pdl(wbmm_tc_dt_kernel<WS, CODES>, dim3(grid), dim3(kDtThreads), lay.total,
                                L.stream, P);
     if (e != cudaSuccess)
         return e;
@@ -716,27 +794,50 @@ long long tc_dt_workspace_floats(const Geom& g)
     return WBMM_DT_COUNTER_WORDS + tc_dt_partials(g) * g.tsz;
 }
 
+bool tc_dt_codes_supported(const Geom& g)
+{
+    return tc_dt_supported(g) && (long long)g.B * g.H * g.W % 16 == 0;
+}
+
+namespace {
+
+template <bool CODES>
+cudaError_t dt_launch(const Geom& g, const void* x, const uint8_t* exps, const void* dy,
+                      float* partials, float* dT, bool after_dx, const Launch& L)
+{
+    switch (g.w) {
+    case 2: return dt_launch_ws<2, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 3: return dt_launch_ws<3, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 4: return dt_launch_ws<4, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 5: return dt_launch_ws<5, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 6: return dt_launch_ws<6, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 7: return dt_launch_ws<7, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 8: return dt_launch_ws<8, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 9: return dt_launch_ws<9, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 10: return dt_launch_ws<10, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 11: return dt_launch_ws<11, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 12: return dt_launch_ws<12, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 13: return dt_launch_ws<13, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 14: return dt_launch_ws<14, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 15: return dt_launch_ws<15, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    case 16: return dt_launch_ws<16, CODES>(g, x, exps, dy, partials, dT, after_dx, L);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
 cudaError_t tc_dt_launch(const Geom& g, const void* x, const void* dy, float* partials, float* dT,
                          bool after_dx, const Launch& L)
 {
-    switch (g.w) {
-    case 2: return dt_launch_ws<2>(g, x, dy, partials, dT, after_dx, L);
-    case 3: return dt_launch_ws<3>(g, x, dy, partials, dT, after_dx, L);
-    case 4: return dt_launch_ws<4>(g, x, dy, partials, dT, after_dx, L);
-    case 5: return dt_launch_ws<5>(g, x, dy, partials, dT, after_dx, L);
-    case 6: return dt_launch_ws<6>(g, x, dy, partials, dT, after_dx, L);
-    case 7: return dt_launch_ws<7>(g, x, dy, partials, dT, after_dx, L);
-    case 8: return dt_launch_ws<8>(g, x, dy, partials, dT, after_dx, L);
-    case 9: return dt_launch_ws<9>(g, x, dy, partials, dT, after_dx, L);
-    case 10: return dt_launch_ws<10>(g, x, dy, partials, dT, after_dx, L);
-    case 11: return dt_launch_ws<11>(g, x, dy, partials, dT, after_dx, L);
-    case 12: return dt_launch_ws<12>(g, x, dy, partials, dT, after_dx, L);
-    case 13: return dt_launch_ws<13>(g, x, dy, partials, dT, after_dx, L);
-    case 14: return dt_launch_ws<14>(g, x, dy, partials, dT, after_dx, L);
-    case 15: return dt_launch_ws<15>(g, x, dy, partials, dT, after_dx, L);
-    case 16: return dt_launch_ws<16>(g, x, dy, partials, dT, after_dx, L);
-    default: return cudaErrorInvalidValue;
-    }
+    return dt_launch<false>(g, x, nullptr, dy, partials, dT, after_dx, L);
+}
+
+cudaError_t tc_dt_codes_launch(const Geom& g, const uint8_t* codes, const uint8_t* exps,
+                               const void* dy, float* partials, float* dT, bool after_dx,
+                               const Launch& L)
+{
+    return dt_launch<true>(g, codes, exps, dy, partials, dT, after_dx, L);
 }
 
 }  // namespace wbmm
