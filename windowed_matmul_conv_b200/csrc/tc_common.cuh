@@ -137,8 +137,8 @@ __device__ __forceinline__ void transform_group(const uint16_t* raw, uint8_t* ds
 }
 
 // transform_group for a group of windows held as 8-bit codes, window n's at
-// byte n * WS * WS of `codes` (WS even: at even bytes) with step[n], window
-// rows q0 <= q < q1 of the lane's RQ.  The restored values are exact in bf16.
+// byte n * WS * WS of `codes` (WS even: at even bytes) with step[n]; window
+// rows Q0 <= q < Q1 of the lane's RQ.  The restored values are exact in bf16.
 template <int WS, int Q0, int Q1>
 __device__ __forceinline__ void transform_group_codes(const uint8_t* codes, const float* step,
                                                       uint8_t* dst, uint32_t sbo, int gi, int nwin,
@@ -160,22 +160,26 @@ __device__ __forceinline__ void transform_group_codes(const uint8_t* codes, cons
         const int r = q * NROW + rs;
         if (r >= WS)
             continue;
-        const uint8_t* src = base + r * WS;
+        // the aligned words that hold the row's codes, shifted to its start
+        constexpr int NW = (WS + (WS % 2 == 0 ? 2 : 3) + 3) / 4;
+        const uint32_t at = smem_u32(base + r * WS);
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(base + r * WS - (at & 3));
+        uint32_t u[NW + 1];
+#pragma unroll
+        for (int k = 0; k < NW; ++k)
+            u[k] = src[k];
+        u[NW] = 0u;
+#pragma unroll
+        for (int k = 0; k < NW; ++k)
+            u[k] = __funnelshift_r(u[k], u[k + 1], 8 * (at & 3));
         uint32_t w[P::RP / 2];
 #pragma unroll
         for (int m = 0; m < P::RP / 2; ++m) {
             w[m] = 0u;
             if (2 * m >= WS)
                 continue;
-            uint32_t a, b;
-            if constexpr (WS % 2 == 0) {
-                const uint32_t u = reinterpret_cast<const uint16_t*>(src)[m];
-                a = __byte_perm(u, 0x4b000000u, 0x7440);
-                b = __byte_perm(u, 0x4b000000u, 0x7441);
-            } else {
-                a = 0x4b000000u | src[2 * m];
-                b = 2 * m + 1 < WS ? 0x4b000000u | src[2 * m + 1] : 0x4b000080u;
-            }
+            const uint32_t a = __byte_perm(u[m / 2], 0x4b000000u, 0x7440 + (2 * m & 3));
+            const uint32_t b = __byte_perm(u[m / 2], 0x4b000000u, 0x7440 + (2 * m + 1 & 3));
             // 2^23 + code, less 2^23 + 128, times the step; upper halves
             const F2 v = mul2(add2({__uint_as_float(a), __uint_as_float(b)},
                                    {-8388736.0f, -8388736.0f}), {st, st});
