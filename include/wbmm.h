@@ -254,10 +254,13 @@ WBMM_API wbmm_status wbmm_checkpoint_restore(const unsigned char *codes,
 
 /*
  * Bytes of device workspace wbmm_backward_checkpoint needs for the table
- * gradient.  It starts with the arrival counters of
- * wbmm_backward_workspace_bytes, under the same rules (zero before the first
- * use, left zero by every call, shared with wbmm_backward's calls).  Returns
- * 0 for invalid shapes.
+ * gradient.  It is laid out as wbmm_backward's (wbmm_backward_workspace_bytes;
+ * arrival counters first), behind which shapes outside the tensor-core kernels
+ * have room for the restored map.  Its prior content does not matter: the call
+ * clears the counters that it uses, and leaves them zero, so a workspace may be
+ * shared with wbmm_backward's calls (zeroed once, as those need it).  Calls
+ * that share a workspace must not overlap on the GPU.  Returns 0 for invalid
+ * shapes.
  */
 WBMM_API size_t wbmm_backward_checkpoint_workspace_bytes(int B, int C, int H, int W, int w,
                                                          wbmm_dtype dt);

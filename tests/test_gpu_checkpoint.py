@@ -216,3 +216,25 @@ def test_training_step_together():
     torch.cuda.synchronize()
     for a, b in zip(out, cap):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("shape", [(5, 6, 56, 56, 14), (64, 256, 28, 28, 14), (2, 3, 35, 49, 7), (1, 3, 14, 28, 14)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_workspace_content_does_not_matter(shape):
+    """Channels split between CTAs and whole ones, both gradients and dT alone,
+    on a workspace full of garbage."""
+    B, C, H, W, w = shape
+    for kind in ("bf16", "fp32"):
+        x, dy = gen((B, C, H, W), 51, kind), gen((B, C, H, W), 52, kind)
+        T = gen((C, (2 * w - 1) ** 2), 53, kind, 0.02)
+        codes, exps = wb.checkpoint(x, w)
+        xh = wb.checkpoint_restore(codes, exps, x.shape, w, x.dtype)
+        n = wb.wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, DT[kind])
+        ws = torch.full((n,), 0x7f, dtype=torch.uint8, device=DEV)
+        for dx in (True, False):
+            want = wb.backward(xh, T, dy, w, need_dx=dx)
+            dX = torch.empty_like(dy) if dx else None
+            dT = torch.empty_like(want[1])
+            wb.wbmm_backward_checkpoint(codes, exps, T, dy, dX, dT, ws, w)
+            assert torch.equal(dT, want[1]) and (not dx or torch.equal(dX, want[0]))
+            ws.fill_(0x7f)

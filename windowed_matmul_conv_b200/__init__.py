@@ -107,11 +107,13 @@ def _check(status):
         raise WbmmError(status)
 
 
+_DTYPES = {torch.bfloat16: WBMM_BF16, torch.float32: WBMM_F32}
+
+
 def _dt(t):
-    if t.dtype == torch.bfloat16:
-        return WBMM_BF16
-    if t.dtype == torch.float32:
-        return WBMM_F32
+    dt = _DTYPES.get(t.dtype)
+    if dt is not None:
+        return dt
     raise TypeError("WBMM tensors must be bfloat16 or float32, got %s" % t.dtype)
 
 
@@ -157,6 +159,29 @@ def _need(name, t, numel, ref, dtype=None):
                     % (name, t.numel(), numel))
 
 
+def _all(dtype, numel, device, *tensors):
+    """True when every tensor given has the dtype, the device index and at
+    least numel elements (the usual case; the caller names the offender)."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.numel() < numel
+                              or t.get_device() != device):
+            return False
+    return True
+
+
+def _ptrs(*tensors):
+    """Addresses of contiguous CUDA tensors that are on one device."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        elif t.is_cuda and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            raise ValueError("WBMM tensors must be contiguous CUDA tensors")
+    return out
+
+
 def _tsz(w):
     return (2 * int(w) - 1) ** 2
 
@@ -164,7 +189,7 @@ def _tsz(w):
 def _map_shape(x):
     if x.dim() != 4:
         raise ValueError("feature maps must be [B, C, H, W]")
-    return tuple(int(v) for v in x.shape)
+    return x.shape
 
 
 def _windows(B, C, H, W, w):
@@ -176,20 +201,33 @@ def _seq_shape(v):
     shape = v.shape
     if len(shape) == 3:
         return shape
+    if len(shape) == 2:
+        return shape[0], shape[1], 1
     if len(shape) < 2:
         raise ValueError("recurrence tensors must be [B, C, L], [B, C, H, W] or [B, C]")
     return shape[0], shape[1], math.prod(shape[2:])
 
 
 def _need_seq(ref, B, C, L, h0, hT, lengths, states, codes=(), exps=()):
-    _need("state in", h0, B * C, ref, torch.float32)
-    _need("state out", hT, B * C, ref, torch.float32)
-    _need("lengths", lengths, B, ref, torch.int32)
-    _need("states", states, wbmm_scan_states_bytes(B, C, L) // 4, ref, torch.float32)
-    for t in codes:
-        _need("codes", t, B * C * L, ref, torch.uint8)
-    for t in exps:
-        _need("exps", t, B * C * -(-L // WBMM_SEQ_GROUP), ref, torch.uint8)
+    dev, f32 = ref.get_device(), torch.float32
+    if not _all(f32, B * C, dev, h0, hT):
+        _need("state in", h0, B * C, ref, f32)
+        _need("state out", hT, B * C, ref, f32)
+    if lengths is not None:
+        _need("lengths", lengths, B, ref, torch.int32)
+    if states is not None:
+        _need("states", states, B * C * _scan_tiles(L), ref, f32)
+    if not (_all(torch.uint8, B * C * L, dev, *codes)
+            and _all(torch.uint8, B * C * -(-L // WBMM_SEQ_GROUP), dev, *exps)):
+        for t in codes:
+            _need("codes", t, B * C * L, ref, torch.uint8)
+        for t in exps:
+            _need("exps", t, B * C * -(-L // WBMM_SEQ_GROUP), ref, torch.uint8)
+
+
+def _scan_tiles(L):
+    """Entries of the states array a row: one per 256 positions."""
+    return -(-L // 256)
 
 
 # --------------------------------------------------------------- entry points
@@ -258,7 +296,7 @@ def wbmm_checkpoint(x, codes, exps, w, stream=None):
     B, C, H, W = _map_shape(x)
     _need("codes", codes, x.numel(), x, torch.uint8)
     _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
-    _check(_lib.wbmm_checkpoint(_p(x), _p(codes), _p(exps), B, C, H, W, int(w), _dt(x),
+    _check(_lib.wbmm_checkpoint(*_ptrs(x, codes, exps), B, C, H, W, int(w), _dt(x),
                                 _stream(stream, x)))
 
 
@@ -266,12 +304,14 @@ def wbmm_checkpoint_restore(codes, exps, x, w, stream=None):
     B, C, H, W = _map_shape(x)
     _need("codes", codes, x.numel(), x, torch.uint8)
     _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
-    _check(_lib.wbmm_checkpoint_restore(_p(codes), _p(exps), _p(x), B, C, H, W, int(w), _dt(x),
+    _check(_lib.wbmm_checkpoint_restore(*_ptrs(codes, exps, x), B, C, H, W, int(w), _dt(x),
                                         _stream(stream, x)))
 
 
 def wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dtype):
-    dt = _dt(torch.empty(0, dtype=dtype))
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError("WBMM tensors must be bfloat16 or float32, got %s" % dtype)
     return int(_lib.wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, int(w), dt))
 
 
@@ -295,14 +335,13 @@ def wbmm_scan_forward(v, g, h0, lengths, y, hT, states, v_codes, v_exps, g_codes
                       stream=None):
     """v, g, y: [B, C, L] or a map [B, C, H, W] (L = H*W); the rest may be None."""
     B, C, L = _seq_shape(v)
-    n = v.numel()
-    _need("g", g, n, v)
-    _need("y", y, n, v)
-    _need_seq(v, B, C, L, h0=h0, hT=hT, lengths=lengths, states=states,
-              codes=(v_codes, g_codes), exps=(v_exps, g_exps))
-    _check(_lib.wbmm_scan_forward(_p(v), _p(g), _p(h0), _p(lengths), _p(y), _p(hT), _p(states),
-                                  _p(v_codes), _p(v_exps), _p(g_codes), _p(g_exps), B, C, L,
-                                  _dt(v), _stream(stream, v)))
+    if not _all(v.dtype, B * C * L, v.get_device(), g, y):
+        _need("g", g, B * C * L, v)
+        _need("y", y, B * C * L, v)
+    _need_seq(v, B, C, L, h0, hT, lengths, states, (v_codes, g_codes), (v_exps, g_exps))
+    _check(_lib.wbmm_scan_forward(
+        *_ptrs(v, g, h0, lengths, y, hT, states, v_codes, v_exps, g_codes, g_exps), B, C, L,
+        _dt(v), _stream(stream, v)))
 
 
 def wbmm_scan_states_bytes(B, C, L):
@@ -311,23 +350,24 @@ def wbmm_scan_states_bytes(B, C, L):
 
 def wbmm_scan_backward(v, g, states, lengths, dY, dhT, dv, dg, dh0, stream=None):
     B, C, L = _seq_shape(dY)
-    for name, t in (("v", v), ("g", g), ("dv", dv), ("dg", dg)):
-        _need(name, t, dY.numel(), dY)
-    _need_seq(dY, B, C, L, h0=dhT, hT=dh0, lengths=lengths, states=states)
-    _check(_lib.wbmm_scan_backward(_p(v), _p(g), _p(states), _p(lengths), _p(dY), _p(dhT), _p(dv),
-                                   _p(dg), _p(dh0), B, C, L, _dt(dY), _stream(stream, dY)))
+    if not _all(dY.dtype, B * C * L, dY.get_device(), v, g, dv, dg):
+        for name, t in (("v", v), ("g", g), ("dv", dv), ("dg", dg)):
+            _need(name, t, B * C * L, dY)
+    _need_seq(dY, B, C, L, dhT, dh0, lengths, states)
+    _check(_lib.wbmm_scan_backward(*_ptrs(v, g, states, lengths, dY, dhT, dv, dg, dh0), B, C, L,
+                                   _dt(dY), _stream(stream, dY)))
 
 
 def wbmm_scan_backward_checkpoint(v_codes, v_exps, g_codes, g_exps, states, lengths, dY, dhT, dv,
                                   dg, dh0, stream=None):
     B, C, L = _seq_shape(dY)
-    for name, t in (("dv", dv), ("dg", dg)):
-        _need(name, t, dY.numel(), dY)
-    _need_seq(dY, B, C, L, h0=dhT, hT=dh0, lengths=lengths, states=states,
-              codes=(v_codes, g_codes), exps=(v_exps, g_exps))
+    if not _all(dY.dtype, B * C * L, dY.get_device(), dv, dg):
+        _need("dv", dv, B * C * L, dY)
+        _need("dg", dg, B * C * L, dY)
+    _need_seq(dY, B, C, L, dhT, dh0, lengths, states, (v_codes, g_codes), (v_exps, g_exps))
     _check(_lib.wbmm_scan_backward_checkpoint(
-        _p(v_codes), _p(v_exps), _p(g_codes), _p(g_exps), _p(states), _p(lengths), _p(dY),
-        _p(dhT), _p(dv), _p(dg), _p(dh0), B, C, L, _dt(dY), _stream(stream, dY)))
+        *_ptrs(v_codes, v_exps, g_codes, g_exps, states, lengths, dY, dhT, dv, dg, dh0), B, C, L,
+        _dt(dY), _stream(stream, dY)))
 
 
 def wbmm_scan_step(v, g, h, y, h_next, stream=None):
@@ -335,12 +375,13 @@ def wbmm_scan_step(v, g, h, y, h_next, stream=None):
     B, C, L = _seq_shape(v)
     if L != 1:
         raise ValueError("a step takes one position: [B, C]")
-    _need("g", g, B * C, v)
-    _need("y", y, B * C, v)
-    _need("h", h, B * C, v, torch.float32)
-    _need("h_next", h_next, B * C, v, torch.float32)
-    _check(_lib.wbmm_scan_step(_p(v), _p(g), _p(h), _p(y), _p(h_next), B, C, _dt(v),
-                               _stream(stream, v)))
+    dev = v.get_device()
+    if not (_all(v.dtype, B * C, dev, g, y) and _all(torch.float32, B * C, dev, h, h_next)):
+        _need("g", g, B * C, v)
+        _need("y", y, B * C, v)
+        _need("h", h, B * C, v, torch.float32)
+        _need("h_next", h_next, B * C, v, torch.float32)
+    _check(_lib.wbmm_scan_step(*_ptrs(v, g, h, y, h_next), B, C, _dt(v), _stream(stream, v)))
 
 
 def wbmm_get_device_status(stream=None):
@@ -438,14 +479,14 @@ def checkpoint(x, w, stream=None):
     [C, B*nh*nw], one power-of-two step per window."""
     B, C, H, W = _map_shape(x)
     n = _windows(B, C, H, W, w) // max(1, C)
-    codes = torch.empty((C, n, x.numel() // max(1, C * n)), dtype=torch.uint8, device=x.device)
-    exps = torch.empty((C, n), dtype=torch.uint8, device=x.device)
+    codes = x.new_empty((C, n, x.numel() // max(1, C * n)), dtype=torch.uint8)
+    exps = x.new_empty((C, n), dtype=torch.uint8)
     wbmm_checkpoint(x, codes, exps, w, stream)
     return codes, exps
 
 
 def checkpoint_restore(codes, exps, shape, w, dtype, stream=None):
-    x = torch.empty(tuple(shape), dtype=dtype, device=codes.device)
+    x = codes.new_empty(shape, dtype=dtype)
     wbmm_checkpoint_restore(codes, exps, x, w, stream)
     return x
 
@@ -454,16 +495,11 @@ def backward_checkpoint(codes, exps, T, dY, w, need_dx=True, need_dt=True, strea
     """backward() with the forward's input as checkpoint() keeps it."""
     B, C, H, W = _map_shape(dY)
     dX = torch.empty_like(dY) if need_dx else None
-    dT = torch.empty((C, (2 * w - 1) ** 2), dtype=torch.float32, device=dY.device) if need_dt else None
+    dT = dY.new_empty((C, (2 * w - 1) ** 2), dtype=torch.float32) if need_dt else None
     ws = None
     if need_dt:
         nbytes = wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dY.dtype)
-        # the arrival counters start at zero; a restored map behind them need not
-        if nbytes == wbmm_backward_workspace_bytes(B, C, H, W, w, dY.dtype):
-            ws = torch.zeros(nbytes // 4, dtype=torch.float32, device=dY.device)
-        else:
-            ws = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=dY.device)
-            ws[:WBMM_DT_COUNTER_WORDS].zero_()
+        ws = dY.new_empty(nbytes, dtype=torch.uint8)
     wbmm_backward_checkpoint(codes, exps, T, dY, dX, dT, ws, w, stream)
     return dX, dT
 
@@ -483,7 +519,7 @@ class ScanSaved(NamedTuple):
 def scan_forward(v, g, h0=None, lengths=None, stream=None):
     """y and the last state [B, C] fp32 of the gated recurrence over [B, C, L]."""
     y = torch.empty_like(v)
-    hT = torch.empty(v.shape[:2], dtype=torch.float32, device=v.device)
+    hT = v.new_empty(v.shape[:2], dtype=torch.float32)
     wbmm_scan_forward(v, g, h0, lengths, y, hT, None, None, None, None, None, stream)
     return y, hT
 
@@ -492,26 +528,22 @@ def scan_forward_train(v, g, h0=None, lengths=None, checkpoint=False, stream=Non
     """scan_forward that also returns what scan_backward needs; with
     `checkpoint` v and g are kept in 8 bits."""
     B, C, L = _seq_shape(v)
-
-    def new(shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=v.device)
-
-    y, hT = torch.empty_like(v), new((B, C), torch.float32)
-    states = new((B, C, wbmm_scan_states_bytes(B, C, L) // max(1, 4 * B * C)), torch.float32)
-    kept = [None] * 4
-    if checkpoint:
-        n = -(-L // WBMM_SEQ_GROUP)
-        kept = [new(s, torch.uint8) for s in ((B, C, L), (B, C, n), (B, C, L), (B, C, n))]
-    wbmm_scan_forward(v, g, h0, lengths, y, hT, states, *kept, stream)
-    if checkpoint:
-        return y, hT, ScanSaved(kept[0], kept[2], kept[1], kept[3], states, lengths)
-    return y, hT, ScanSaved(v, g, None, None, states, lengths)
+    y, hT = torch.empty_like(v), v.new_empty((B, C), dtype=torch.float32)
+    states = v.new_empty((B, C, _scan_tiles(L)), dtype=torch.float32)
+    if not checkpoint:
+        wbmm_scan_forward(v, g, h0, lengths, y, hT, states, None, None, None, None, stream)
+        return y, hT, ScanSaved(v, g, None, None, states, lengths)
+    v_codes, g_codes = (torch.empty_like(v, dtype=torch.uint8) for _ in range(2))
+    v_exps, g_exps = (v.new_empty((B, C, -(-L // WBMM_SEQ_GROUP)), dtype=torch.uint8)
+                      for _ in range(2))
+    wbmm_scan_forward(v, g, h0, lengths, y, hT, states, v_codes, v_exps, g_codes, g_exps, stream)
+    return y, hT, ScanSaved(v_codes, g_codes, v_exps, g_exps, states, lengths)
 
 
 def scan_backward(saved, dY, dhT=None, stream=None):
     """dv, dg and dh0 [B, C] fp32 from scan_forward_train's `saved`."""
     dv, dg = torch.empty_like(dY), torch.empty_like(dY)
-    dh0 = torch.empty(dY.shape[:2], dtype=torch.float32, device=dY.device)
+    dh0 = dY.new_empty(dY.shape[:2], dtype=torch.float32)
     if saved.v_exps is None:
         wbmm_scan_backward(saved.v, saved.g, saved.states, saved.lengths, dY, dhT, dv, dg, dh0,
                            stream)

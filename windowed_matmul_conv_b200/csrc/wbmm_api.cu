@@ -198,7 +198,7 @@ bool reads_codes(const Geom& g, wbmm_dtype dt)
 // where it is null codes and exps, is used by the table gradient only.
 wbmm_status backward_run(const Geom& g, const void* x, const unsigned char* codes,
                          const unsigned char* exps, const void* T, const void* dY, void* dX,
-                         float* dT, void* workspace, wbmm_dtype dt, const Launch& L)
+                         float* dT, void* workspace, bool clear, wbmm_dtype dt, const Launch& L)
 {
     wbmm_status st = WBMM_OK;
     const bool tc_dt = dT && dt == WBMM_BF16 && tc_dt_supported(g);
@@ -215,6 +215,11 @@ wbmm_status backward_run(const Geom& g, const void* x, const unsigned char* code
         Lx.num_sms = (2 * L.num_sms + 2) / 5;
         Lt.num_sms = L.num_sms - Lx.num_sms;
     }
+    // a checkpoint call takes its workspace as it is: the counters that the
+    // launch uses are cleared here, ahead of the two kernels
+    if (tc_dt && clear && tc_dt_splits_channels(g, Lt.num_sms) &&
+        cudaMemsetAsync(workspace, 0, (size_t)g.C * 4, L.stream) != cudaSuccess)
+        return WBMM_ERR_CUDA;
     if (dX) {
         if (dt == WBMM_BF16 && tc_toep_supported(g)) {
             st = from_cuda(tc_toep_launch(g, kTableFlip, dY, T, dX, Lx));
@@ -429,7 +434,7 @@ wbmm_status wbmm_backward(const void* x, const void* T, const void* dY, void* dX
     Launch L;
     if ((st = make_launch(stream, &L)) != WBMM_OK)
         return st;
-    return backward_run(g, x, nullptr, nullptr, T, dY, dX, dT, workspace, dt, L);
+    return backward_run(g, x, nullptr, nullptr, T, dY, dX, dT, workspace, false, dt, L);
 }
 
 wbmm_status wbmm_cache_matrices(const void* T, void* M, int C, int w, wbmm_dtype dt,
@@ -638,7 +643,7 @@ wbmm_status wbmm_backward_checkpoint(const unsigned char* codes, const unsigned 
         if (st != WBMM_OK)
             return st;
     }
-    return backward_run(g, x, codes, exps, T, dY, dX, dT, workspace, dt, L);
+    return backward_run(g, x, codes, exps, T, dY, dX, dT, workspace, true, dt, L);
 }
 
 size_t wbmm_scan_states_bytes(int B, int C, int L)

@@ -93,6 +93,10 @@ long long tc_dt_workspace_floats(const Geom& g);
 cudaError_t tc_dt_launch(const Geom& g, const void* x, const void* dy, float* workspace, float* dT,
                          bool after_dx, const Launch& L);
 
+// Whether a launch on num_sms SMs splits channels between CTAs, and so counts
+// arrivals in the workspace.
+bool tc_dt_splits_channels(const Geom& g, int num_sms);
+
 // The same with x as an 8-bit checkpoint (a channel's codes a multiple of 16
 // bytes); equal, bit for bit, to tc_dt_launch on the restored map.
 bool tc_dt_codes_supported(const Geom& g);

@@ -684,6 +684,34 @@ long long tc_dt_partials_impl(const Geom& g)
     return g.C + (tiles < kDtMaxGrid ? tiles : kDtMaxGrid) - 1;
 }
 
+// How the tiles are split into one range per CTA: rq + (k < rr) units of
+// `unit` tiles for CTA k.
+struct DtSplit {
+    int grid, unit, rq, rr;
+};
+
+DtSplit dt_split(const Geom& g, int num_sms)
+{
+    DtSplit s;
+    const int tpc = dt_tiles_per_channel(g), tiles = g.C * tpc;
+    s.grid = num_sms < kDtMaxGrid ? num_sms : kDtMaxGrid;
+    if (s.grid > tiles)
+        s.grid = tiles;
+    s.unit = s.rq = s.rr = 0;
+    if (s.grid < 1)
+        return s;
+    // Ranges of whole channels when that costs a CTA no more tiles than the
+    // tile-granular split (no channel is then shared between CTAs: one
+    // reduction of G per channel, no partial tables), else tile ranges.
+    const int per_tile = (tiles + s.grid - 1) / s.grid;
+    const int per_chan = (g.C + s.grid - 1) / s.grid * tpc;
+    s.unit = g.C >= s.grid && per_chan <= per_tile ? tpc : 1;
+    const int units = s.unit == 1 ? tiles : g.C;
+    s.rq = units / s.grid;
+    s.rr = units - s.rq * s.grid;
+    return s;
+}
+
 template <int WS, bool CODES>
 cudaError_t dt_launch_ws(const Geom& g, const void* x, const uint8_t* exps, const void* dy,
                          float* workspace, float* dT, bool after_dx, const Launch& L)
@@ -715,26 +743,13 @@ cudaError_t dt_launch_ws(const Geom& g, const void* x, const uint8_t* exps, cons
     P.bpt = F::NT / g.nw;
     P.bands = (int)g.bands;
     P.tpc = (P.bands + P.bpt - 1) / P.bpt;
-    const int tiles = g.C * P.tpc;
-    int grid = L.num_sms < kDtMaxGrid ? L.num_sms : kDtMaxGrid;
-    if (grid > tiles)
-        grid = tiles;
+    const DtSplit split = dt_split(g, L.num_sms);
+    const int grid = split.grid;
     if (grid < 1)
         return cudaSuccess;
-    // Ranges of whole channels when that costs a CTA no more tiles than the
-    // tile-granular split (no channel is then shared between CTAs: one
-    // reduction of G per channel, no partial tables), else tile ranges.
-    const int per_tile = (tiles + grid - 1) / grid;
-    const int per_chan = (g.C + grid - 1) / grid * P.tpc;
-    if (g.C >= grid && per_chan <= per_tile) {
-        P.unit = P.tpc;
-        P.rq = g.C / grid;
-        P.rr = g.C - P.rq * grid;
-    } else {
-        P.unit = 1;
-        P.rq = tiles / grid;
-        P.rr = tiles - P.rq * grid;
-    }
+    P.unit = split.unit;
+    P.rq = split.rq;
+    P.rr = split.rr;
     P.dep_wait = after_dx ? 0 : 1;
     P.use_tmap = 0;
     P.kimg = 0;
@@ -792,6 +807,11 @@ long long tc_dt_workspace_floats(const Geom& g)
     // every shape, so a workspace shared by calls of different shapes keeps
     // them zero), then the partial tables
     return WBMM_DT_COUNTER_WORDS + tc_dt_partials(g) * g.tsz;
+}
+
+bool tc_dt_splits_channels(const Geom& g, int num_sms)
+{
+    return dt_split(g, num_sms).unit == 1;
 }
 
 bool tc_dt_codes_supported(const Geom& g)
