@@ -321,29 +321,61 @@ struct Steps {
     }
 };
 
-// The reversed steps c = f (dy + c') of a lane's positions.
+// The reversed steps c = f (dy + c') of a lane's positions, in two parts: the
+// gates and the composed map, and, once the state before and the c behind the
+// lane's tile are known, the gradients, for which v and dy are read again.
 template <typename T, bool CODES>
-struct BackSteps : Steps<T, CODES> {
-    F2 d[4], fd[4];
-    float D;
-    __device__ __forceinline__ void make(const Inputs<T, CODES>& in, const Raw<T>& dy, int cnt)
+struct BackSteps {
+    F2 f[4], i[4];
+    float A, D;
+    __device__ __forceinline__ void make(const std::conditional_t<CODES, RawCodes, Raw<T>>& g,
+                                         const Raw<T>& dy, int cnt)
     {
-        Steps<T, CODES>::make(in, cnt);
+        F2 x[4], d[4];
+        gate_values8<T>(g, x);
         unpack8(dy, d);
-        if (cnt < 8)
-            cut8(d, cnt, 0.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            fd[j] = mul2(this->f[j], d[j]);
-        D = fmaf(this->f[3].x, fd[3].y, fd[3].x);
+            gate2<T>(x[j], f[j], i[j]);
+        if (cnt < 8) {
+            cut8(f, cnt, 1.0f);
+            cut8(i, cnt, 0.0f);
+            cut8(d, cnt, 0.0f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            d[j] = mul2(f[j], d[j]);
+        D = fmaf(f[3].x, d[3].y, d[3].x);
+        A = f[0].x * f[0].y;
 #pragma unroll
         for (int j = 2; j >= 0; --j)
-            D = fmaf(this->f[j].x, fmaf(this->f[j].y, D, fd[j].y), fd[j].x);
+            D = fmaf(f[j].x, fmaf(f[j].y, D, d[j].y), d[j].x);
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+            A = A * f[j].x * f[j].y;
     }
-    // dv and dg from the state s before the lane and the c behind it
-    __device__ __forceinline__ void grads(float s, float c, int cnt, F2 (&ov)[4], F2 (&og)[4]) const
+    // dv and dg from the state `h` before all S lanes and the c behind this one
+    template <int S>
+    __device__ __forceinline__ void grads(const std::conditional_t<CODES, RawCodes, Raw<T>>& rv,
+                                          const Raw<T>& dy, float h, float c, int cnt, int sub,
+                                          F2 (&ov)[4], F2 (&og)[4]) const
     {
-        const auto &f = this->f, &i = this->i, &u = this->u, &v = this->v;
+        F2 v[4], d[4], u[4];
+        values8<T>(rv, v);
+        unpack8(dy, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            u[j] = mul2(i[j], v[j]);
+        if (cnt < 8) {
+            cut8(u, cnt, 0.0f);
+            cut8(d, cnt, 0.0f);
+        }
+        float a = A, H = fmaf(f[0].y, u[0].x, u[0].y), end;
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+            H = fmaf(f[j].y, fmaf(f[j].x, H, u[j].x), u[j].y);
+        lane_scan<S, false>(a, H, sub);
+        float s = lane_start<S, false>(a, H, h, sub, end);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float s1 = fmaf(f[j].x, s, u[j].x);
@@ -353,11 +385,12 @@ struct BackSteps : Steps<T, CODES> {
         }
 #pragma unroll
         for (int j = 3; j >= 0; --j) {
-            const float c1 = fmaf(f[j].y, c, fd[j].y);
+            const F2 fd = mul2(f[j], d[j]);
+            const float c1 = fmaf(f[j].y, c, fd.y);
             const F2 dh = add2(d[j], {c1, c});
             ov[j] = mul2(dh, i[j]);
             og[j] = mul2(og[j], ov[j]);
-            c = fmaf(f[j].x, c1, fd[j].x);
+            c = fmaf(f[j].x, c1, fd.x);
         }
         if (cnt < 8) {
             // i is 0 past the sequence's end, but NaN of a state times 0 is not
@@ -561,14 +594,20 @@ constexpr int kImage = 256 * (int)sizeof(T) + 48;
 constexpr int kWarps = 4;
 
 // One stage: v and g (maps or codes), dy.
-template <typename T, bool VEC, bool CODES, bool BACK>
+template <typename T, bool VEC, bool CODES, bool BACK, bool TEAM>
 struct Stage {
     static constexpr int MAP = VEC ? 256 * (int)sizeof(T) : kImage<T>;
     static constexpr int ARR = !CODES ? MAP : VEC ? 256 : 304;
     static constexpr int DY = 2 * ARR;
     static constexpr int BYTES = DY + (BACK ? MAP : 0);
-    // four stages, three of the larger fp32 ones
-    static constexpr int DEPTH = BYTES > 2048 ? 3 : 4;
+    // four stages; three of the larger fp32 ones where a warp works alone
+    // (more warps fit an SM: B32 C256 L1568 forward 32.0 us, 34.0 with four)
+    // and where four would not fit (fp32 backward)
+    static constexpr int DEPTH = BYTES > (TEAM ? 3072 : 2048) ? 3 : 4;
+    // tiles a round: a team's warp takes two, whose arithmetic overlaps and
+    // which share the round's barrier, where the ring holds two rounds (768
+    // rows of 50176 forward 43.0 us, 57.5 with one)
+    static constexpr int PER = TEAM && DEPTH == 4 ? 2 : 1;
     static constexpr int OUT = VEC ? 0 : kImage<T>;     // image of an output
     static constexpr int WARP = DEPTH * BYTES + OUT;
 };
@@ -691,11 +730,11 @@ struct RowWalk {
     long long row;
     int n;              // positions of the sequence
     int ntile, ngrp;    // of the row
-    int step, from;     // every step-th tile from the from-th on
+    int step, from;     // a round's tiles: from every step-th on, the first of them the from-th
     int rounds;
 };
 
-template <bool TEAM>
+template <bool TEAM, int PER>
 __device__ __forceinline__ RowWalk row_walk(const ScanArgs& P, const Team& M)
 {
     RowWalk w;
@@ -704,8 +743,8 @@ __device__ __forceinline__ RowWalk row_walk(const ScanArgs& P, const Team& M)
     w.n = w.row < P.rows ? row_len(P.lengths, w.row, P.C, P.L) : 0;
     w.ntile = (int)((P.L + kScanTile - 1ll) / kScanTile);
     w.ngrp = (int)((P.L + WBMM_SEQ_GROUP - 1ll) / WBMM_SEQ_GROUP);
-    w.step = TEAM ? M.size : 1;
-    w.from = TEAM ? M.me : 0;
+    w.step = (TEAM ? M.size : 1) * PER;
+    w.from = TEAM ? M.me * PER : 0;
     w.rounds = (w.ntile + w.step - 1) / w.step;
     return w;
 }
@@ -763,8 +802,8 @@ __device__ __forceinline__ int lane_count(int left, int lane)
 template <typename T, bool VEC, bool KEEP, bool TEAM>
 __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const ScanArgs P)
 {
-    using G = Stage<T, VEC, false, false>;
-    constexpr int SZ = (int)sizeof(T);
+    using G = Stage<T, VEC, false, false, TEAM>;
+    constexpr int SZ = (int)sizeof(T), PER = G::PER;
     __shared__ __align__(16) uint8_t ring[kWarps][G::WARP];
     __shared__ float2 slots[2][TEAM ? kTeamMax : 1];
     grid_dep_wait();
@@ -775,99 +814,126 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const ScanArgs P)
     Team M = {};
     if constexpr (TEAM)
         M.init(reinterpret_cast<float2(*)[kTeamMax]>(slots));
-    const RowWalk w = row_walk<TEAM>(P, M);
+    const RowWalk w = row_walk<TEAM, PER>(P, M);
     if (w.row >= P.rows)
         return;         // no teams: they have a row each
     const long long base = w.row * P.L, elems = P.rows * P.L;
-    long long at = base + (long long)w.from * kScanTile;    // the tile's first element
+    long long at = base + (long long)w.from * kScanTile;    // the round's first element
     const int off_v = shift_of<SZ, VEC>(P.v, at), off_g = shift_of<SZ, VEC>(P.g, at);
     Stream<SZ, VEC> fv, fg;
     fv.start(P.v, at, lane);
     fg.start(P.g, at, lane);
     const int hop = w.step * kScanTile;
-    int left = w.n - w.from * kScanTile;            // from the tile's start to the sequence's end
+    int left = w.n - w.from * kScanTile;        // from the round's start to the sequence's end
     int far = left, stored = P.L - w.from * kScanTile;
-    uint8_t* into = mine;                           // the stage to fetch into
+    int turn = 0;                               // tile of its round that is fetched next
+    uint8_t* into = mine;                       // the stage to fetch into
     const uint8_t* const last = mine + (G::DEPTH - 1) * G::BYTES;
     auto prefetch = [&] {
         if (far > 0) {
             fv.fetch(into, far, far >= kScanTile + 16, P.v, elems, lane);
             fg.fetch(into + G::ARR, far, far >= kScanTile + 16, P.g, elems, lane);
         }
-        fv.advance(w.step);
-        fg.advance(w.step);
-        far -= hop;
+        const int go = PER == 1 || turn == PER - 1 ? w.step - (PER - 1) : 1;
+        turn = turn == PER - 1 ? 0 : turn + 1;
+        fv.advance(go);
+        fg.advance(go);
+        far -= go * kScanTile;
         into = into == last ? mine : into + G::BYTES;
         cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < G::DEPTH - 1; ++k)
+    for (int k = 0; k < G::DEPTH - PER; ++k)
         prefetch();
     float h = P.h0 ? P.h0[w.row] : 0.0f;
-    float kept = 0.0f;      // lane k: the state before the k-th of 32 rounds' tiles
+    float kept = 0.0f;      // lane k: the state before the k-th of 32 tiles
     const uint8_t* st = mine;
     for (int k = 0; k < w.rounds; ++k) {
         if constexpr (!VEC)
-            __syncwarp();       // every lane has read the stage that is fetched into next
-        prefetch();
-        cp_async_wait_group<G::DEPTH - 1>();
+            __syncwarp();       // every lane has read the stages that are fetched into next
+#pragma unroll
+        for (int m = 0; m < PER; ++m)
+            prefetch();
+        cp_async_wait_group<G::DEPTH - PER>();
         if constexpr (!VEC)
             __syncwarp();
-        const int cnt = left >= kScanTile ? 8 : lane_count(left, lane);
-        Inputs<T, false> in;
-        in.v = stage_map<T, VEC>(st, off_v, lane);
-        in.g = stage_map<T, VEC>(st + G::ARR, off_g, lane);
-        st = st == last ? mine : st + G::BYTES;
-        Steps<T, false> s8;
-        s8.make(in, cnt);
-        float A = s8.A, H = s8.H, hin = h, end;
-        lane_scan<32, false>(A, H, lane);
+        Inputs<T, false> in[PER];
+        Steps<T, false> s8[PER];
+        float A[PER], H[PER];
+        int cnt[PER];
+#pragma unroll
+        for (int m = 0; m < PER; ++m) {
+            cnt[m] = left >= (m + 1) * kScanTile ? 8 : lane_count(left - m * kScanTile, lane);
+            in[m].v = stage_map<T, VEC>(st, off_v, lane);
+            in[m].g = stage_map<T, VEC>(st + G::ARR, off_g, lane);
+            st = st == last ? mine : st + G::BYTES;
+            s8[m].make(in[m], cnt[m]);
+            A[m] = s8[m].A;
+            H[m] = s8[m].H;
+        }
+#pragma unroll
+        for (int m = 0; m < PER; ++m)
+            lane_scan<32, false>(A[m], H[m], lane);
+        float hin = h;
         if constexpr (TEAM) {
-            M.publish(k & 1, __shfl_sync(kFull, A, 31), __shfl_sync(kFull, H, 31), lane);
+            static_assert(PER == 2, "forward stages are small enough for four");
+            const float a0 = __shfl_sync(kFull, A[0], 31), h0 = __shfl_sync(kFull, H[0], 31);
+            const float a1 = __shfl_sync(kFull, A[1], 31), h1 = __shfl_sync(kFull, H[1], 31);
+            M.publish(k & 1, a0 * a1, fmaf(a1, h0, h1), lane);
             hin = M.join<false>(k & 1, h);
         }
-        const float s = lane_start<32, false>(A, H, hin, lane, end);
-        if constexpr (!TEAM)
-            h = __shfl_sync(kFull, end, 31);
-        F2 y[4];
-        s8.replay(s, y);
-        if (cnt < 8)
-            cut8(y, cnt, 0.0f);
-        tile_store<T, VEC>(static_cast<T*>(P.y) + at, stored, y, out, lane);
-        if constexpr (KEEP) {
-            if (stored > 0) {
-                const int all = lane_count(stored, lane);
-                const long long grp = w.row * w.ngrp + (long long)(k * w.step + w.from) * 4 + lane / 8;
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    F2 x[4];
-                    values8<T>(a ? in.g : in.v, x);
-                    if (cnt < 8)
-                        cut8(x, cnt, 0.0f);
-                    uint2 code;
-                    const uint32_t e = encode8<32>(x, code);
-                    uint8_t* p = (a ? P.g_codes : P.v_codes) + at;
-                    if constexpr (VEC) {
-                        if (all > 0)
-                            *reinterpret_cast<uint2*>(p + lane * 8) = code;
-                    } else {
-                        image_store_codes<true>(p, stored < kScanTile ? stored : kScanTile, lane * 8, 8,
-                                                code, out, lane);
+        for (int m = 0; m < PER; ++m) {
+            const int here = stored - m * kScanTile;
+            float end;
+            const float s = lane_start<32, false>(A[m], H[m], hin, lane, end);
+            const float hnext = !TEAM || m + 1 < PER ? __shfl_sync(kFull, end, 31) : 0.0f;
+            F2 y[4];
+            s8[m].replay(s, y);
+            if (cnt[m] < 8)
+                cut8(y, cnt[m], 0.0f);
+            tile_store<T, VEC>(static_cast<T*>(P.y) + at + m * kScanTile, here, y, out, lane);
+            const int t = k * w.step + w.from + m;
+            if constexpr (KEEP) {
+                if (here > 0) {
+                    const int all = lane_count(here, lane);
+                    const long long grp = w.row * w.ngrp + (long long)t * 4 + lane / 8;
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        F2 x[4];
+                        values8<T>(a ? in[m].g : in[m].v, x);
+                        if (cnt[m] < 8)
+                            cut8(x, cnt[m], 0.0f);
+                        uint2 code;
+                        const uint32_t e = encode8<32>(x, code);
+                        uint8_t* p = (a ? P.g_codes : P.v_codes) + at + m * kScanTile;
+                        if constexpr (VEC) {
+                            if (all > 0)
+                                *reinterpret_cast<uint2*>(p + lane * 8) = code;
+                        } else {
+                            image_store_codes<true>(p, here < kScanTile ? here : kScanTile, lane * 8, 8,
+                                                    code, out, lane);
+                        }
+                        if (all > 0 && (lane & 7) == 0)
+                            (a ? P.g_exps : P.v_exps)[grp] = (uint8_t)e;
                     }
-                    if (all > 0 && (lane & 7) == 0)
-                        (a ? P.g_exps : P.v_exps)[grp] = (uint8_t)e;
                 }
             }
-        }
-        if (P.states) {
-            if (lane == (k & 31))
-                kept = hin;
-            if ((k & 31) == 31 || k == w.rounds - 1) {
-                const int t = ((k & ~31) + lane) * w.step + w.from;
-                if (lane <= (k & 31) && (long long)t * kScanTile < w.n)
-                    P.states[w.row * w.ntile + t] = kept;
+            if (P.states) {
+                const int q = k * PER + m;
+                if (lane == (q & 31))
+                    kept = hin;
+                if ((q & 31) == 31 || (k == w.rounds - 1 && m == PER - 1)) {
+                    const int i = (q & ~31) + lane;
+                    const int ti = i / PER * w.step + w.from + i % PER;
+                    if (lane <= (q & 31) && (long long)ti * kScanTile < w.n)
+                        P.states[w.row * w.ntile + ti] = kept;
+                }
             }
+            hin = hnext;
         }
+        if constexpr (!TEAM)
+            h = hin;
         left -= hop;
         stored -= hop;
         at += hop;
@@ -881,8 +947,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const ScanArgs P)
 template <typename T, bool VEC, bool CODES, bool TEAM>
 __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
 {
-    using G = Stage<T, VEC, CODES, true>;
-    constexpr int SZ = (int)sizeof(T), IN = CODES ? 1 : SZ;
+    using G = Stage<T, VEC, CODES, true, TEAM>;
+    constexpr int SZ = (int)sizeof(T), IN = CODES ? 1 : SZ, PER = G::PER;
     __shared__ __align__(16) uint8_t ring[kWarps][G::WARP];
     __shared__ float2 slots[2][TEAM ? kTeamMax : 1];
     grid_dep_wait();
@@ -893,11 +959,12 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
     Team M = {};
     if constexpr (TEAM)
         M.init(reinterpret_cast<float2(*)[kTeamMax]>(slots));
-    const RowWalk w = row_walk<TEAM>(P, M);
+    const RowWalk w = row_walk<TEAM, PER>(P, M);
     if (w.row >= P.rows)
         return;         // no teams: they have a row each
     const long long base = w.row * P.L, elems = P.rows * P.L;
-    const int t_last = (w.rounds - 1) * w.step + w.from;
+    // the last tile of the round that is taken first
+    const int t_last = (w.rounds - 1) * w.step + w.from + PER - 1;
     long long at = base + (long long)t_last * kScanTile;
     const void* const sv = CODES ? P.v_codes : P.v;
     const void* const sg = CODES ? P.g_codes : P.g;
@@ -911,7 +978,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
     const int hop = w.step * kScanTile;
     int left = (int)(w.n - (long long)t_last * kScanTile);
     int far = left, stored = (int)(P.L - (long long)t_last * kScanTile);
-    int togo = w.rounds;                            // tiles to fetch
+    int togo = w.rounds * PER;                      // tiles to fetch
+    int turn = 0;                                   // tile of its round that is fetched next
     uint8_t* into = mine;
     const uint8_t* const last = mine + (G::DEPTH - 1) * G::BYTES;
     auto prefetch = [&] {
@@ -920,26 +988,28 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
             fg.fetch(into + G::ARR, far, far >= kScanTile + 16, sg, elems, lane);
             fd.fetch(into + G::DY, far, far >= kScanTile + 16, P.dy, elems, lane);
         }
-        fv.advance(-w.step);
-        fg.advance(-w.step);
-        fd.advance(-w.step);
-        far += togo > 0 ? hop : 0;
+        const int go = PER == 1 || turn == PER - 1 ? w.step - (PER - 1) : 1;
+        turn = turn == PER - 1 ? 0 : turn + 1;
+        fv.advance(-go);
+        fg.advance(-go);
+        fd.advance(-go);
+        far += togo > 0 ? go * kScanTile : 0;
         --togo;
         into = into == last ? mine : into + G::BYTES;
         cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < G::DEPTH - 1; ++k)
+    for (int k = 0; k < G::DEPTH - PER; ++k)
         prefetch();
     float c = P.h0 ? P.h0[w.row] : 0.0f;
     // lane k: the state before the tile, and the exponent bytes, of the k-th of
-    // 32 rounds
+    // 32 tiles
     float states = 0.0f;
     uint32_t ve = 0, ge = 0;
     const uint8_t* st = mine;
     for (int k = 0; k < w.rounds; ++k) {
-        if ((k & 31) == 0) {
-            const int t = t_last - (k + lane) * w.step;
+        if ((k * PER & 31) == 0) {
+            const int q = k * PER + lane, t = t_last - q / PER * w.step - q % PER;
             states = t >= 0 && (long long)t * kScanTile < w.n ? __ldg(P.states + w.row * w.ntile + t) : 0.0f;
             if constexpr (CODES) {
                 ve = tile_exps(P.v_exps + w.row * w.ngrp, t, w.ngrp);
@@ -947,49 +1017,73 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
             }
         }
         if constexpr (!VEC)
-            __syncwarp();       // every lane has read the stage that is fetched into next
-        prefetch();
-        cp_async_wait_group<G::DEPTH - 1>();
+            __syncwarp();       // every lane has read the stages that are fetched into next
+#pragma unroll
+        for (int m = 0; m < PER; ++m)
+            prefetch();
+        cp_async_wait_group<G::DEPTH - PER>();
         if constexpr (!VEC)
             __syncwarp();
-        const int cnt = left >= kScanTile ? 8 : lane_count(left, lane);
-        Inputs<T, CODES> in;
-        if constexpr (CODES) {
-            if constexpr (VEC) {
-                in.v.w = *reinterpret_cast<const uint2*>(st + 8 * lane);
-                in.g.w = *reinterpret_cast<const uint2*>(st + G::ARR + 8 * lane);
+        BackSteps<T, CODES> s8[PER];
+        float A[PER], D[PER];
+        int cnt[PER];
+        const uint8_t* from[PER];
+        auto input = [&](int m, bool gates) {
+            std::conditional_t<CODES, RawCodes, Raw<T>> r;
+            const uint8_t* p = from[m] + (gates ? G::ARR : 0);
+            const int off = gates ? off_g : off_v;
+            if constexpr (CODES) {
+                if constexpr (VEC)
+                    r.w = *reinterpret_cast<const uint2*>(p + 8 * lane);
+                else
+                    r.w = image_codes(p, off + 8 * lane);
+                r.e = __byte_perm(__shfl_sync(kFull, gates ? ge : ve, (k * PER + m) & 31), 0u,
+                                  0x4440 + lane / 8);
             } else {
-                in.v.w = image_codes(st, off_v + 8 * lane);
-                in.g.w = image_codes(st + G::ARR, off_g + 8 * lane);
+                r = stage_map<T, VEC>(p, off, lane);
             }
-            const uint32_t sel = 0x4440 + lane / 8;
-            in.v.e = __byte_perm(__shfl_sync(kFull, ve, k & 31), 0u, sel);
-            in.g.e = __byte_perm(__shfl_sync(kFull, ge, k & 31), 0u, sel);
-        } else {
-            in.v = stage_map<T, VEC>(st, off_v, lane);
-            in.g = stage_map<T, VEC>(st + G::ARR, off_g, lane);
+            return r;
+        };
+#pragma unroll
+        for (int m = 0; m < PER; ++m) {
+            const int here = left + m * kScanTile;
+            cnt[m] = here >= kScanTile ? 8 : lane_count(here, lane);
+            from[m] = st;
+            st = st == last ? mine : st + G::BYTES;
+            s8[m].make(input(m, true), stage_map<T, VEC>(from[m] + G::DY, off_d, lane), cnt[m]);
+            A[m] = s8[m].A;
+            D[m] = s8[m].D;
         }
-        const Raw<T> dy = stage_map<T, VEC>(st + G::DY, off_d, lane);
-        st = st == last ? mine : st + G::BYTES;
-        const float h = __shfl_sync(kFull, states, k & 31);
-        BackSteps<T, CODES> s8;
-        s8.make(in, dy, cnt);
-        float A = s8.A, D = s8.D, cin = c, end;
-        lane_scan<32, true>(A, D, lane);
+#pragma unroll
+        for (int m = 0; m < PER; ++m)
+            lane_scan<32, true>(A[m], D[m], lane);
+        float cin = c;
         if constexpr (TEAM) {
-            M.publish(k & 1, __shfl_sync(kFull, A, 0), __shfl_sync(kFull, D, 0), lane);
+            const float a0 = __shfl_sync(kFull, A[0], 0), d0 = __shfl_sync(kFull, D[0], 0);
+            if constexpr (PER == 1) {
+                M.publish(k & 1, a0, d0, lane);
+            } else {
+                const float a1 = __shfl_sync(kFull, A[PER - 1], 0), d1 = __shfl_sync(kFull, D[PER - 1], 0);
+                M.publish(k & 1, a0 * a1, fmaf(a1, d0, d1), lane);
+            }
             cin = M.join<true>(k & 1, c);
         }
-        const float cc = lane_start<32, true>(A, D, cin, lane, end);
+#pragma unroll
+        for (int m = 0; m < PER; ++m) {
+            float end;
+            const float cc = lane_start<32, true>(A[m], D[m], cin, lane, end);
+            cin = !TEAM || m + 1 < PER ? __shfl_sync(kFull, end, 0) : 0.0f;
+            const float h = __shfl_sync(kFull, states, (k * PER + m) & 31);
+            F2 ov[4], og[4];
+            s8[m].template grads<32>(input(m, false), stage_map<T, VEC>(from[m] + G::DY, off_d, lane), h, cc,
+                                     cnt[m], lane, ov, og);
+            const long long to = at - m * kScanTile;
+            const int here = stored + m * kScanTile;
+            tile_store<T, VEC>(static_cast<T*>(P.dv) + to, here, ov, out, lane);
+            tile_store<T, VEC>(static_cast<T*>(P.dg) + to, here, og, out, lane);
+        }
         if constexpr (!TEAM)
-            c = __shfl_sync(kFull, end, 0);
-        float A2 = s8.A, H = s8.H;
-        lane_scan<32, false>(A2, H, lane);
-        const float s = lane_start<32, false>(A2, H, h, lane, end);
-        F2 ov[4], og[4];
-        s8.grads(s, cc, cnt, ov, og);
-        tile_store<T, VEC>(static_cast<T*>(P.dv) + at, stored, ov, out, lane);
-        tile_store<T, VEC>(static_cast<T*>(P.dg) + at, stored, og, out, lane);
+            c = cin;
         left += hop;
         stored += hop;
         at -= hop;
@@ -1178,15 +1272,12 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_short_kernel(const ScanA
     const float c = P.h0 && w.L > 0 ? P.h0[w.row] : 0.0f;
     const float h = w.n > 0 ? __ldg(P.states + w.row) : 0.0f;
     BackSteps<T, CODES> s8;
-    s8.make(in, dy, w.cnt);
-    float A = s8.A, D = s8.D, end, after;
+    s8.make(in.g, dy, w.cnt);
+    float A = s8.A, D = s8.D, end;
     lane_scan<S, true>(A, D, w.sub);
     const float cc = lane_start<S, true>(A, D, c, w.sub, end);
-    float A2 = s8.A, H = s8.H;
-    lane_scan<S, false>(A2, H, w.sub);
-    const float s = lane_start<S, false>(A2, H, h, w.sub, after);
     F2 ov[4], og[4];
-    s8.grads(s, cc, w.cnt, ov, og);
+    s8.template grads<S>(in.v, dy, h, cc, w.cnt, w.sub, ov, og);
     group_store<T, VEC>(static_cast<T*>(P.dv), w, first, ov, img, lane);
     group_store<T, VEC>(static_cast<T*>(P.dg), w, first, og, img, lane);
     if (P.hT && w.sub == 0 && w.L > 0)
