@@ -323,7 +323,7 @@ struct Steps {
 
 // The reversed steps c = f (dy + c') of a lane's positions, in two parts: the
 // gates and the composed map, and, once the state before and the c behind the
-// lane's tile are known, the gradients, for which v and dy are read again.
+// lane's tile are known, the gradients, for which v is read.
 template <typename T, bool CODES>
 struct BackSteps {
     F2 f[4], i[4];
@@ -1027,7 +1027,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
         BackSteps<T, CODES> s8[PER];
         float A[PER], D[PER];
         int cnt[PER];
-        const uint8_t* from[PER];
+        const uint8_t* from[PER] = {};
+        Raw<T> dy[PER];
         auto input = [&](int m, bool gates) {
             std::conditional_t<CODES, RawCodes, Raw<T>> r;
             const uint8_t* p = from[m] + (gates ? G::ARR : 0);
@@ -1050,7 +1051,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
             cnt[m] = here >= kScanTile ? 8 : lane_count(here, lane);
             from[m] = st;
             st = st == last ? mine : st + G::BYTES;
-            s8[m].make(input(m, true), stage_map<T, VEC>(from[m] + G::DY, off_d, lane), cnt[m]);
+            dy[m] = stage_map<T, VEC>(from[m] + G::DY, off_d, lane);
+            s8[m].make(input(m, true), dy[m], cnt[m]);
             A[m] = s8[m].A;
             D[m] = s8[m].D;
         }
@@ -1075,8 +1077,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
             cin = !TEAM || m + 1 < PER ? __shfl_sync(kFull, end, 0) : 0.0f;
             const float h = __shfl_sync(kFull, states, (k * PER + m) & 31);
             F2 ov[4], og[4];
-            s8[m].template grads<32>(input(m, false), stage_map<T, VEC>(from[m] + G::DY, off_d, lane), h, cc,
-                                     cnt[m], lane, ov, og);
+            s8[m].template grads<32>(input(m, false), dy[m], h, cc, cnt[m], lane, ov, og);
             const long long to = at - m * kScanTile;
             const int here = stored + m * kScanTile;
             tile_store<T, VEC>(static_cast<T*>(P.dv) + to, here, ov, out, lane);
