@@ -77,7 +77,7 @@ def check_train(d, kind, checkpoint):
     assert torch.equal(dv, again[0]) and torch.equal(dg, again[1]) and torch.equal(dh0, again[2])
 
 
-LENGTHS = [1, 2, 7, 8, 9, 31, 32, 33, 63, 64, 65, 127, 128, 129, 196, 255, 256, 257, 512, 777, 1024, 2049]
+LENGTHS = [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 127, 128, 129, 196, 255, 256, 257, 512, 777, 1024, 2049]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
@@ -98,7 +98,7 @@ def test_few_and_many_rows(shape, kind, checkpoint):
 
 @pytest.mark.parametrize("checkpoint", [False, True])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
-@pytest.mark.parametrize("L", [1, 5, 30, 100, 256, 1000, 4104])
+@pytest.mark.parametrize("L", [1, 5, 13, 30, 60, 64, 100, 256, 1000, 4104])
 def test_padded_batch(L, kind, checkpoint):
     check_train(make(5, 4, L, kind, 100 + L, carry=L % 8 == 0, ragged=True), kind, checkpoint)
 

@@ -437,50 +437,70 @@ __device__ __forceinline__ void image_copy(uint8_t* dst, const uint8_t* at, int 
     }
 }
 
-// N words from byte `off` of an image, off % 4 == 0 or (two-byte elements)
-// 2, the same for all lanes but for multiples of 16.
-template <int N, bool HALVES>
-__device__ __forceinline__ void shifted(const uint8_t* img, int off, uint32_t (&r)[N])
+// N words from byte sh on of a block of an image, sh the same for all lanes
+// and even, 0 <= sh < 16.  Eight words (fp32) are taken from where they are in
+// one of four uniform branches; four words are moved down in two steps, which
+// costs less than the branches.
+template <int N>
+__device__ __forceinline__ void shifted(const uint8_t* block, int sh, uint32_t (&r)[N])
 {
     uint32_t u[N + 4];
-    const uint8_t* p = img + (off & ~15);
 #pragma unroll
     for (int k = 0; k < N + 4; k += 4) {
-        const uint4 q = lds4(p + 4 * k);
-        u[k] = q.x; u[k + 1] = q.y; u[k + 2] = q.z; u[k + 3] = q.w;
+        if (N == 4 || k < N || sh != 0) {
+            const uint4 q = lds4(block + 4 * k);
+            u[k] = q.x; u[k + 1] = q.y; u[k + 2] = q.z; u[k + 3] = q.w;
+        } else {
+            u[k] = u[k + 1] = u[k + 2] = u[k + 3] = 0u;
+        }
     }
-    if (off & 8) {
+    if constexpr (N == 4) {
+        if (sh & 8) {
 #pragma unroll
-        for (int k = 0; k < N + 2; ++k)
-            u[k] = u[k + 2];
+            for (int k = 0; k < N + 2; ++k)
+                u[k] = u[k + 2];
+        }
+        if (sh & 4) {
+#pragma unroll
+            for (int k = 0; k < N + 1; ++k)
+                u[k] = u[k + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            r[k] = sh & 2 ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
+    } else {
+        auto take = [&](auto from) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                r[k] = u[decltype(from)::value + k];
+        };
+        if (sh < 8) {
+            if (sh < 4)
+                take(std::integral_constant<int, 0>());
+            else
+                take(std::integral_constant<int, 1>());
+        } else {
+            if (sh < 12)
+                take(std::integral_constant<int, 2>());
+            else
+                take(std::integral_constant<int, 3>());
+        }
     }
-    if (off & 4) {
-#pragma unroll
-        for (int k = 0; k < N + 1; ++k)
-            u[k] = u[k + 1];
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-        r[k] = HALVES && (off & 2) ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
 }
 
 // Eight elements at byte `off` of an image.
-template <typename T, bool ONE_ROW>
+template <typename T>
 __device__ __forceinline__ Raw<T> image_read(const uint8_t* img, int off)
 {
     Raw<T> r;
-    if constexpr (ONE_ROW) {
-        shifted<Raw<T>::N, sizeof(T) == 2>(img, off, r.w);
-    } else {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(img + (off & ~3));
-        uint32_t u[Raw<T>::N + 1];
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(img + (off & ~3));
+    uint32_t u[Raw<T>::N + 1];
 #pragma unroll
-        for (int k = 0; k < Raw<T>::N + 1; ++k)
-            u[k] = p[k];
+    for (int k = 0; k < Raw<T>::N + 1; ++k)
+        u[k] = p[k];
 #pragma unroll
-        for (int k = 0; k < Raw<T>::N; ++k)
-            r.w[k] = sizeof(T) == 2 && (off & 2) ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
-    }
+    for (int k = 0; k < Raw<T>::N; ++k)
+        r.w[k] = sizeof(T) == 2 && (off & 2) ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
     return r;
 }
 
@@ -518,7 +538,7 @@ __device__ __forceinline__ void image_store(T* p, int count, int mine, int cnt, 
                 if (k == 0 && s != 0)
                     continue;
                 uint32_t q[4];
-                shifted<4, sizeof(T) == 2>(stage, (E + k * E - s) * (int)sizeof(T), q);
+                shifted<4>(stage + 16 * (s == 0 ? k + 1 : k), (16 - s * (int)sizeof(T)) & 15, q);
                 *reinterpret_cast<uint4*>(p + k * E - s) = make_uint4(q[0], q[1], q[2], q[3]);
             }
             if (s != 0) {
@@ -553,33 +573,55 @@ __device__ __forceinline__ void image_store(T* p, int count, int mine, int cnt, 
     }
 }
 
-// The same for codes: aligned words of memory, single bytes at the ends.
+// The same for codes: 16-byte blocks of a whole tile of one row, else words;
+// single bytes at the ends.
 template <bool ONE_ROW>
 __device__ __forceinline__ void image_store_codes(uint8_t* p, int count, int mine, int cnt, uint2 codes,
                                                   uint8_t* stage, int lane)
 {
-    const int s = (int)(reinterpret_cast<uintptr_t>(p) & 3);
     __syncwarp();
     if constexpr (ONE_ROW) {
-        *reinterpret_cast<uint2*>(stage + 8 + mine) = codes;
+        *reinterpret_cast<uint2*>(stage + 16 + mine) = codes;
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j < cnt)
-                stage[8 + mine + j] = (uint8_t)((j < 4 ? codes.x : codes.y) >> (8 * (j & 3)));
+                stage[16 + mine + j] = (uint8_t)((j < 4 ? codes.x : codes.y) >> (8 * (j & 3)));
     }
     __syncwarp();
+    if (ONE_ROW && count == kScanTile) {
+        const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+        if (lane < 16 && (lane > 0 || s == 0)) {
+            const int off = 16 + 16 * lane - s, sh = 8 * (off & 3);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + (off & ~3));
+            uint32_t u[5];
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+                u[k] = w[k];
+            *reinterpret_cast<uint4*>(p + 16 * lane - s) =
+                make_uint4(__funnelshift_r(u[0], u[1], sh), __funnelshift_r(u[1], u[2], sh),
+                           __funnelshift_r(u[2], u[3], sh), __funnelshift_r(u[3], u[4], sh));
+        }
+        if (s != 0) {
+            const bool low = lane < 16 - s;
+            const int e = low ? lane : kScanTile - 32 + lane;
+            if (low || lane >= 32 - s)
+                p[e] = stage[16 + e];
+        }
+        return;
+    }
+    const int s = (int)(reinterpret_cast<uintptr_t>(p) & 3);
     const int words = (s + count + 3) / 4;
     for (int k = lane; k < words; k += 32) {
         const int e0 = 4 * k - s;
         if (e0 >= 0 && e0 + 4 <= count) {
-            const int off = 8 + e0;
+            const int off = 16 + e0;
             const uint32_t* w = reinterpret_cast<const uint32_t*>(stage + (off & ~3));
             *reinterpret_cast<uint32_t*>(p + e0) = __funnelshift_r(w[0], w[1], 8 * (off & 3));
         } else {
             for (int j = 0; j < 4; ++j)
                 if (e0 + j >= 0 && e0 + j < count)
-                    p[e0 + j] = stage[8 + e0 + j];
+                    p[e0 + j] = stage[16 + e0 + j];
         }
     }
 }
@@ -760,7 +802,7 @@ __device__ __forceinline__ Raw<T> stage_map(const uint8_t* st, int off, int lane
             r.w[k] = q.x; r.w[k + 1] = q.y; r.w[k + 2] = q.z; r.w[k + 3] = q.w;
         }
     } else {
-        r = image_read<T, true>(st, off + lane * 8 * (int)sizeof(T));
+        shifted<Raw<T>::N>(st + lane * 8 * (int)sizeof(T), off, r.w);
     }
     return r;
 }
@@ -1094,8 +1136,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
 }
 
 // ---------------------------------------------------------------- short rows
-// Rows of at most 8 S positions: S = 1, 4 or 16 lanes a row, 32 / S rows a
-// warp, which are neighbours in memory.
+// Rows of at most 8 S positions: S = 1, 2, 4, 8 or 16 lanes a row, 32 / S rows
+// a warp, which are neighbours in memory.
 template <int S>
 struct Group {
     long long row0, row;    // the warp's first row; this lane's
@@ -1144,7 +1186,7 @@ __device__ __forceinline__ Raw<T> group_map(const uint8_t* img, const void* base
             }
         }
     } else {
-        r = image_read<T, false>(img, (int)(reinterpret_cast<uintptr_t>(p) & 15) + mine * (int)sizeof(T));
+        r = image_read<T>(img, (int)(reinterpret_cast<uintptr_t>(p) & 15) + mine * (int)sizeof(T));
     }
     return r;
 }
@@ -1402,10 +1444,15 @@ int team_for(long long rows, int L, int num_sms)
 template <typename T, bool VEC, bool AUX>
 cudaError_t lanes_launch(const ScanArgs& A, bool backward, const Launch& L)
 {
+    // as few lanes as hold a row in one tile
     if (A.L <= 8)
         return short_launch<T, 1, VEC, AUX>(A, backward, L);
+    if (A.L <= 16)
+        return short_launch<T, 2, VEC, AUX>(A, backward, L);
     if (A.L <= 32)
         return short_launch<T, 4, VEC, AUX>(A, backward, L);
+    if (A.L <= 64)
+        return short_launch<T, 8, VEC, AUX>(A, backward, L);
     if (A.L <= 128)
         return short_launch<T, 16, VEC, AUX>(A, backward, L);
     const int team = team_for(A.rows, A.L, L.num_sms);
