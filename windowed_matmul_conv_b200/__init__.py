@@ -129,9 +129,11 @@ def _stream(stream, ref=None):
     """Stream handle for a call whose maps live on ``ref``'s device.  The
     library launches on the current device, so ``ref`` and the stream must
     be on it."""
-    if stream is None and ref is not None and ref.get_device() == torch.cuda.current_device():
+    if stream is None and ref is not None:
         # the current device's current stream, without the stream object
-        return torch._C._cuda_getCurrentRawStream(ref.get_device())
+        d = ref.get_device()
+        if d == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(d)
     s = torch.cuda.current_stream() if stream is None else stream
     if ref is not None:
         d, cur = ref.get_device(), torch.cuda.current_device()
@@ -170,12 +172,13 @@ def _all(dtype, numel, device, *tensors):
 
 
 def _ptrs(*tensors):
-    """Addresses of contiguous CUDA tensors that are on one device."""
+    """Addresses of tensors that are on one device (checked): CUDA, contiguous."""
     out = []
+    cuda = tensors[0].is_cuda
     for t in tensors:
         if t is None:
             out.append(None)
-        elif t.is_cuda and t.is_contiguous():
+        elif cuda and t.is_contiguous():
             out.append(t.data_ptr())
         else:
             raise ValueError("WBMM tensors must be contiguous CUDA tensors")

@@ -13,6 +13,15 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr uint32_t kExpBad = 255u;      // exponent byte of a group with a NaN or infinity
 constexpr uint32_t kExpTop = 248u;      // the largest of the others, 2^121
 
+// The larger of two bf16 magnitudes, pairwise; NaN (bits above infinity's)
+// where either is.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Exponent byte of a group whose largest |x| has the fp32 bits `top` (NaN
 // sorts above infinity, and both above every finite value).  127 steps have
 // to reach |x| after rounding, i.e. |x| < 127.5 steps: with |x| = m 2^k,

@@ -176,7 +176,7 @@ struct RowVals {
         uint32_t m = 0;
 #pragma unroll
         for (int t = 0; t < N; ++t)
-            m = F32 ? max(m, u[t] & kAbsMask) : __vmaxu2(m, u[t] & 0x7fff7fffu);
+            m = F32 ? max(m, u[t] & kAbsMask) : max_abs2(m, u[t] & 0x7fff7fffu);
         return F32 ? m : max(m & 0xffff0000u, m << 16);
     }
     __device__ __forceinline__ float value(int t) const

@@ -196,36 +196,86 @@ __device__ __forceinline__ void decode8(const RawCodes& r, F2 (&x)[4])
     }
 }
 
-// 8-bit form of 64 successive positions: 8 lanes of 8 (all the row's lanes
-// where it has fewer).  Returns the group's exponent byte.
-template <int S>
-__device__ __forceinline__ uint32_t encode8(const F2 (&x)[4], uint2& codes)
+// The codes of a lane's 8 values in a group with exponent byte e.
+__device__ __forceinline__ uint2 codes8(const F2 (&x)[4], uint32_t e)
 {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t a = __float_as_uint(x[j].x) & kAbsMask, b = __float_as_uint(x[j].y) & kAbsMask;
-        top = max(top, max(a, b));
-    }
-#pragma unroll
-    for (int o = 1; o < (S < 8 ? S : 8); o <<= 1)
-        top = max(top, __shfl_xor_sync(kFull, top, o));
-    const uint32_t e = group_exp(top);
     const float inv = inv_step_of(e);
     uint32_t q[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        F2 v = x[j];
-        if (e >= kExpTop)
-            v = {group_fix(v.x, e), group_fix(v.y, e)};
         // as quant_code: the product is exact, so one rounding
-        const F2 r = fma2(v, {inv, inv}, {12583040.0f, 12583040.0f});
+        const F2 r = fma2(x[j], {inv, inv}, {12583040.0f, 12583040.0f});
         q[2 * j] = __float_as_uint(r.x);
         q[2 * j + 1] = __float_as_uint(r.y);
     }
-    codes.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-    codes.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-    return e;
+    return make_uint2(
+        __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+        __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+}
+
+// 8-bit forms of v and g over 64 successive positions: 8 lanes of 8 (all the
+// row's lanes where it has fewer); positions from cnt on count as zero.
+// Exponent bytes in ev and eg.  bf16 magnitudes are compared in pairs,
+// and the groups' of v and g in one word.
+template <int S, typename T>
+__device__ __forceinline__ void encode8(const Raw<T>& rv, const Raw<T>& rg, int cnt, uint2& cv, uint2& cg,
+                                        uint32_t& ev, uint32_t& eg)
+{
+    F2 v[4], g[4];
+    unpack8(rv, v);
+    unpack8(rg, g);
+    if (cnt < 8) {
+        cut8(v, cnt, 0.0f);
+        cut8(g, cnt, 0.0f);
+    }
+    constexpr int LANES = S < 8 ? S : 8;
+    if constexpr (sizeof(T) == 2) {
+        uint32_t mv = 0, mg = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t wv = rv.w[j], wg = rg.w[j];
+            if (cnt < 8) {
+                const uint32_t keep = (2 * j < cnt ? 0xffffu : 0u) | (2 * j + 1 < cnt ? 0xffff0000u : 0u);
+                wv &= keep;
+                wg &= keep;
+            }
+            mv = max_abs2(mv, wv & 0x7fff7fffu);
+            mg = max_abs2(mg, wg & 0x7fff7fffu);
+        }
+        // v's largest in the lower half, g's in the upper
+        uint32_t m = max_abs2(__byte_perm(mv, mg, 0x5410), __byte_perm(mv, mg, 0x7632));
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+            m = max_abs2(m, __shfl_xor_sync(kFull, m, o));
+        ev = group_exp(m << 16);
+        eg = group_exp(m & 0xffff0000u);
+    } else {
+        uint32_t mv = 0, mg = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            mv = max(mv, max(__float_as_uint(v[j].x) & kAbsMask, __float_as_uint(v[j].y) & kAbsMask));
+            mg = max(mg, max(__float_as_uint(g[j].x) & kAbsMask, __float_as_uint(g[j].y) & kAbsMask));
+        }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) {
+            mv = max(mv, __shfl_xor_sync(kFull, mv, o));
+            mg = max(mg, __shfl_xor_sync(kFull, mg, o));
+        }
+        ev = group_exp(mv);
+        eg = group_exp(mg);
+    }
+    if (max(ev, eg) >= kExpTop) {
+        // rare: a bad group, or one at the top of the range
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (ev >= kExpTop)
+                v[j] = {group_fix(v[j].x, ev), group_fix(v[j].y, ev)};
+            if (eg >= kExpTop)
+                g[j] = {group_fix(g[j].x, eg), group_fix(g[j].y, eg)};
+        }
+    }
+    cv = codes8(v, ev);
+    cg = codes8(g, eg);
 }
 
 // What a lane reads of one tile besides dy.
@@ -830,10 +880,22 @@ __device__ __forceinline__ int lane_count(int left, int lane)
     return c < 0 ? 0 : c > 8 ? 8 : c;
 }
 
+// Blocks an SM that the register allocation has to leave room for: measured on
+// 8192 rows of 3136 (forward 27.6 us with 8, 28.4 unconstrained; with
+// checkpoints 43.0 with 8; backward 44.0 with 6, 45.1 with 7), 768 rows of
+// 50176 (a team's forward 44.4 us with 6, 52.5 with 4) and 128 rows of 65536
+// (with checkpoints 23.8 us with 4, 27.3 with 5; backward 23.6 and 26.7).
+constexpr int fwd_blocks(bool vec, bool keep, bool team)
+{
+    return team ? (vec && !keep ? 6 : 4) : vec || !keep ? 8 : 6;
+}
+constexpr int bwd_blocks(bool vec, bool team) { return team ? 4 : vec ? 6 : 5; }
+
 // Forward: one row a warp, or (TEAM) a CTA or cluster.  KEEP: the 8-bit forms
 // of v and g are written too.
 template <typename T, bool VEC, bool KEEP, bool TEAM>
-__global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const ScanArgs P)
+__global__ void __launch_bounds__(32 * kWarps, fwd_blocks(VEC, KEEP, TEAM))
+    scan_fwd_kernel(const ScanArgs P)
 {
     using G = Stage<T, VEC, false, false, TEAM>;
     constexpr int SZ = (int)sizeof(T), PER = G::PER;
@@ -930,25 +992,24 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const ScanArgs P)
             if constexpr (KEEP) {
                 if (here > 0) {
                     const int all = lane_count(here, lane);
-                    const long long grp = w.row * w.ngrp + (long long)t * 4 + lane / 8;
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        F2 x[4];
-                        values8<T>(a ? in[m].g : in[m].v, x);
-                        if (cnt[m] < 8)
-                            cut8(x, cnt[m], 0.0f);
-                        uint2 code;
-                        const uint32_t e = encode8<32>(x, code);
-                        uint8_t* p = (a ? P.g_codes : P.v_codes) + at + m * kScanTile;
-                        if constexpr (VEC) {
-                            if (all > 0)
-                                *reinterpret_cast<uint2*>(p + lane * 8) = code;
-                        } else {
-                            image_store_codes<true>(p, here < kScanTile ? here : kScanTile, lane * 8, 8,
-                                                    code, out, lane);
+                    const long long to = at + m * kScanTile;
+                    uint2 cv, cg;
+                    uint32_t ev, eg;
+                    encode8<32>(in[m].v, in[m].g, cnt[m], cv, cg, ev, eg);
+                    if constexpr (VEC) {
+                        if (all > 0) {
+                            *reinterpret_cast<uint2*>(P.v_codes + to + lane * 8) = cv;
+                            *reinterpret_cast<uint2*>(P.g_codes + to + lane * 8) = cg;
                         }
-                        if (all > 0 && (lane & 7) == 0)
-                            (a ? P.g_exps : P.v_exps)[grp] = (uint8_t)e;
+                    } else {
+                        const int n = here < kScanTile ? here : kScanTile;
+                        image_store_codes<true>(P.v_codes + to, n, lane * 8, 8, cv, out, lane);
+                        image_store_codes<true>(P.g_codes + to, n, lane * 8, 8, cg, out, lane);
+                    }
+                    if (all > 0 && (lane & 7) == 0) {
+                        const long long grp = w.row * w.ngrp + (long long)t * 4 + lane / 8;
+                        P.v_exps[grp] = (uint8_t)ev;
+                        P.g_exps[grp] = (uint8_t)eg;
                     }
                 }
             }
@@ -978,7 +1039,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const ScanArgs P)
 // Backward, tiles from the last to the first.  CODES: v and g from their
 // 8-bit forms.
 template <typename T, bool VEC, bool CODES, bool TEAM>
-__global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const ScanArgs P)
+__global__ void __launch_bounds__(32 * kWarps, bwd_blocks(VEC, TEAM))
+    scan_bwd_kernel(const ScanArgs P)
 {
     using G = Stage<T, VEC, CODES, true, TEAM>;
     constexpr int SZ = (int)sizeof(T), IN = CODES ? 1 : SZ, PER = G::PER;
@@ -1252,23 +1314,23 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_short_kernel(const ScanA
         cut8(y, w.cnt, 0.0f);
     group_store<T, VEC>(static_cast<T*>(P.y), w, first, y, img, lane);
     if constexpr (KEEP) {
-        const int ngrp = (P.L + WBMM_SEQ_GROUP - 1) / WBMM_SEQ_GROUP;
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            F2 x[4];
-            values8<T>(a ? in.g : in.v, x);
-            cut8(x, w.cnt, 0.0f);
-            uint2 code;
-            const uint32_t e = encode8<S>(x, code);
-            uint8_t* p = (a ? P.g_codes : P.v_codes) + first;
-            if constexpr (VEC) {
-                if (w.all > 0)
-                    *reinterpret_cast<uint2*>(p + w.mine) = code;
-            } else {
-                image_store_codes<S == 32>(p, w.count, w.mine, w.all, code, img, lane);
+        uint2 cv, cg;
+        uint32_t ev, eg;
+        encode8<S>(in.v, in.g, w.cnt, cv, cg, ev, eg);
+        if constexpr (VEC) {
+            if (w.all > 0) {
+                *reinterpret_cast<uint2*>(P.v_codes + first + w.mine) = cv;
+                *reinterpret_cast<uint2*>(P.g_codes + first + w.mine) = cg;
             }
-            if (w.all > 0 && (w.sub & 7) == 0)
-                (a ? P.g_exps : P.v_exps)[w.row * ngrp + w.sub / 8] = (uint8_t)e;
+        } else {
+            image_store_codes<S == 32>(P.v_codes + first, w.count, w.mine, w.all, cv, img, lane);
+            image_store_codes<S == 32>(P.g_codes + first, w.count, w.mine, w.all, cg, img, lane);
+        }
+        if (w.all > 0 && (w.sub & 7) == 0) {
+            const int ngrp = (P.L + WBMM_SEQ_GROUP - 1) / WBMM_SEQ_GROUP;
+            const long long grp = w.row * ngrp + w.sub / 8;
+            P.v_exps[grp] = (uint8_t)ev;
+            P.g_exps[grp] = (uint8_t)eg;
         }
     }
     if (P.states && w.sub == 0 && w.n > 0)
