@@ -99,7 +99,8 @@ def test_checkpoint_guards():
 
 BWD_SHAPES = [s for s in SHAPES if s[4] in (2, 3, 5, 7, 8, 13, 14, 16)] + [
     (2, 2, 28, 28, 28), (5, 2, 105, 112, 7), (4, 2, 39, 104, 13), (2, 2, 24, 96, 12), (3, 3, 48, 64, 16),
-    (1, 9, 7, 56, 7), (3, 5, 7, 8, 1), (2, 2, 63, 63, 9), (5, 3, 42, 28, 14), (1, 3, 14, 28, 14)]
+    (1, 9, 7, 56, 7), (3, 5, 7, 8, 1), (2, 2, 63, 63, 9), (5, 3, 42, 28, 14), (1, 3, 14, 28, 14)] + [
+    (3, 2, 2 * w, 8 * w, w) for w in range(2, 17)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
@@ -238,3 +239,24 @@ def test_workspace_content_does_not_matter(shape):
             wb.wbmm_backward_checkpoint(codes, exps, T, dy, dX, dT, ws, w)
             assert torch.equal(dT, want[1]) and (not dx or torch.equal(dX, want[0]))
             ws.fill_(0x7f)
+
+
+def test_offsets_past_32_bits():
+    """A map of more than 2^31 elements: the codes of its last image, and the
+    table gradient of the whole."""
+    B, C, H, W, w = 700, 64, 224, 224, 14
+    x = torch.zeros((B, C, H, W), dtype=torch.bfloat16, device=DEV)
+    x[-1] = gen((1, C, H, W), 61, "bf16")[0]
+    codes, exps = wb.checkpoint(x, w)
+    want = wb.checkpoint(x[-1:].contiguous(), w)
+    n = (H // w) * (W // w)
+    assert torch.equal(codes[:, -n:], want[0]) and torch.equal(exps[:, -n:], want[1])
+    assert (codes[:, :-n] == 128).all() and (exps[:, :-n] == 1).all()
+    back = wb.checkpoint_restore(codes, exps, x.shape, w, x.dtype)
+    assert torch.equal(back[-1:], wb.checkpoint_restore(*want, (1, C, H, W), w, x.dtype))
+    assert (back[:-1] == 0).all()
+    dy = torch.zeros_like(x)
+    dy[-1] = gen((1, C, H, W), 62, "bf16")[0]
+    _, dT = wb.backward_checkpoint(codes, exps, None, dy, w, need_dx=False)
+    _, pT = wb.backward(back, None, dy, w, need_dx=False)
+    assert torch.equal(dT, pT) and dT.abs().max() > 0

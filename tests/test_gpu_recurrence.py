@@ -36,6 +36,8 @@ def make(B, C, L, kind, seed, carry=True, ragged=False, gate=1.0):
         n = torch.randint(0, L + 1, (B,), generator=gen, dtype=torch.int32)
         n[0] = 0
         n[-1] = L + 5                      # taken as L
+        if B > 3:
+            n[1] = -7                      # taken as 0
         d["lengths"] = n
     return {k: t.to(DEV) if t is not None else None for k, t in d.items()}
 
@@ -320,3 +322,54 @@ def test_offsets_past_32_bits():
     want, last = wb.scan_forward(tail["v"], tail["g"])
     assert torch.equal(y[0, 2, -4096:], want[0, 0]) and torch.equal(hT[0, 2], last[0, 0])
     assert (y[0, 2, :-4096] == 0).all() and (hT[0, :2] == 0).all()
+
+
+@pytest.mark.parametrize("shape", [(2, 3, 5), (2, 3, 200), (2, 3, 300), (1, 2, 9000), (40, 50, 700)])
+def test_states_updated_in_place(shape):
+    """hT in h0's buffer and dh0 in dhT's, whichever kernel takes the rows."""
+    d = make(*shape, "bf16", 101)
+    y, hT, saved = wb.scan_forward_train(d["v"], d["g"], d["h0"])
+    dv, dg, dh0 = wb.scan_backward(saved, d["dY"], d["dhT"])
+    for _ in range(3):
+        h, c, y2, dv2, dg2 = d["h0"].clone(), d["dhT"].clone(), *(torch.empty_like(y) for _ in range(3))
+        wb.wbmm_scan_forward(d["v"], d["g"], h, None, y2, h, saved.states, None, None, None, None)
+        wb.wbmm_scan_backward(d["v"], d["g"], saved.states, None, d["dY"], c, dv2, dg2, c)
+        for a, b in ((h, hT), (y2, y), (c, dh0), (dv2, dv), (dg2, dg)):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU share nothing."""
+    ds = [make(1, 8, 30000 + 8 * k, "bf16", 111 + k) for k in range(2)]
+    want = []
+    for d in ds:
+        y, hT, saved = wb.scan_forward_train(d["v"], d["g"], d["h0"], checkpoint=True)
+        want.append((y, hT) + wb.scan_backward(saved, d["dY"], d["dhT"]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    got = []
+    for _ in range(5):
+        for d, s in zip(ds, streams):
+            with torch.cuda.stream(s):
+                y, hT, saved = wb.scan_forward_train(d["v"], d["g"], d["h0"], checkpoint=True)
+                got.append((y, hT) + wb.scan_backward(saved, d["dY"], d["dhT"]))
+    torch.cuda.synchronize()
+    for k, g in enumerate(got):
+        for a, b in zip(g, want[k % 2]):
+            assert torch.equal(a, b)
+
+
+def test_saved_of_another_shape_is_refused():
+    d = make(2, 3, 40, "bf16", 121)
+    saved = wb.scan_forward_train(d["v"], d["g"])[2]
+    before = wb.wbmm_launch_count()
+    for dY in (d["dY"][:, :, :32].contiguous(), d["dY"].reshape(3, 2, 40)):
+        with pytest.raises(wb.WbmmError) as e:
+            wb.scan_backward(saved, dY)
+        assert e.value.status == 1
+    with pytest.raises(ValueError):
+        wb.scan_forward(d["v"].transpose(0, 1), d["g"].transpose(0, 1))
+    with pytest.raises(wb.WbmmError) as e:      # bf16 rows that start between 16-byte boundaries
+        wb.scan_forward(d["v"].reshape(-1)[1:41].view(1, 1, 40), d["g"].reshape(-1)[1:41].view(1, 1, 40))
+    assert e.value.status == 4
+    assert wb.wbmm_launch_count() == before

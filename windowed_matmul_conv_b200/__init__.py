@@ -545,6 +545,9 @@ def scan_forward_train(v, g, h0=None, lengths=None, checkpoint=False, stream=Non
 
 def scan_backward(saved, dY, dhT=None, stream=None):
     """dv, dg and dh0 [B, C] fp32 from scan_forward_train's `saved`."""
+    if saved.v.numel() != dY.numel() or saved.v.shape[:2] != dY.shape[:2]:
+        raise WbmmError(WBMM_ERR_INVALID_ARG, "dY is %s, the forward call's maps were %s"
+                        % (tuple(dY.shape), tuple(saved.v.shape)))
     dv, dg = torch.empty_like(dY), torch.empty_like(dY)
     dh0 = dY.new_empty(dY.shape[:2], dtype=torch.float32)
     if saved.v_exps is None:
