@@ -477,20 +477,31 @@ def dw3x3(y, K, stream=None):
     return z
 
 
+# The following allocate their outputs, so they check the caller's buffers only
+# and pass the new ones' addresses as they are.
+
 def checkpoint(x, w, stream=None):
     """8-bit form of a map: codes [C, B*nh*nw, w*w] and exponent bytes
     [C, B*nh*nw], one power-of-two step per window."""
     B, C, H, W = _map_shape(x)
+    px, = _ptrs(x)
     n = _windows(B, C, H, W, w) // max(1, C)
     codes = x.new_empty((C, n, x.numel() // max(1, C * n)), dtype=torch.uint8)
     exps = x.new_empty((C, n), dtype=torch.uint8)
-    wbmm_checkpoint(x, codes, exps, w, stream)
+    _check(_lib.wbmm_checkpoint(px, codes.data_ptr(), exps.data_ptr(), B, C, H, W, int(w), _dt(x),
+                                _stream(stream, x)))
     return codes, exps
 
 
 def checkpoint_restore(codes, exps, shape, w, dtype, stream=None):
+    """The map of the given shape and dtype that checkpoint() stored."""
+    B, C, H, W = shape
     x = codes.new_empty(shape, dtype=dtype)
-    wbmm_checkpoint_restore(codes, exps, x, w, stream)
+    _need("codes", codes, B * C * H * W, x, torch.uint8)
+    _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
+    pc, pe = _ptrs(codes, exps)
+    _check(_lib.wbmm_checkpoint_restore(pc, pe, x.data_ptr(), B, C, H, W, int(w), _dt(x),
+                                        _stream(stream, x)))
     return x
 
 
@@ -519,48 +530,81 @@ class ScanSaved(NamedTuple):
     lengths: Optional[torch.Tensor]
 
 
+def _scan_inputs(v, g, h0, lengths):
+    """Sizes of a forward call and the addresses of its checked inputs."""
+    B, C, L = _seq_shape(v)
+    if not _all(v.dtype, B * C * L, v.get_device(), g):
+        _need("g", g, B * C * L, v)
+    if h0 is not None:
+        _need("h0", h0, B * C, v, torch.float32)
+    if lengths is not None:
+        _need("lengths", lengths, B, v, torch.int32)
+    return B, C, L, _ptrs(v, g, h0, lengths)
+
+
 def scan_forward(v, g, h0=None, lengths=None, stream=None):
     """y and the last state [B, C] fp32 of the gated recurrence over [B, C, L]."""
-    y = torch.empty_like(v)
-    hT = v.new_empty(v.shape[:2], dtype=torch.float32)
-    wbmm_scan_forward(v, g, h0, lengths, y, hT, None, None, None, None, None, stream)
+    B, C, L, inputs = _scan_inputs(v, g, h0, lengths)
+    y, hT = torch.empty_like(v), v.new_empty((B, C), dtype=torch.float32)
+    _check(_lib.wbmm_scan_forward(*inputs, y.data_ptr(), hT.data_ptr(), None, None, None, None,
+                                  None, B, C, L, _dt(v), _stream(stream, v)))
     return y, hT
 
 
 def scan_forward_train(v, g, h0=None, lengths=None, checkpoint=False, stream=None):
     """scan_forward that also returns what scan_backward needs; with
     `checkpoint` v and g are kept in 8 bits."""
-    B, C, L = _seq_shape(v)
+    B, C, L, inputs = _scan_inputs(v, g, h0, lengths)
     y, hT = torch.empty_like(v), v.new_empty((B, C), dtype=torch.float32)
     states = v.new_empty((B, C, _scan_tiles(L)), dtype=torch.float32)
-    if not checkpoint:
-        wbmm_scan_forward(v, g, h0, lengths, y, hT, states, None, None, None, None, stream)
-        return y, hT, ScanSaved(v, g, None, None, states, lengths)
-    v_codes, g_codes = (torch.empty_like(v, dtype=torch.uint8) for _ in range(2))
-    v_exps, g_exps = (v.new_empty((B, C, -(-L // WBMM_SEQ_GROUP)), dtype=torch.uint8)
-                      for _ in range(2))
-    wbmm_scan_forward(v, g, h0, lengths, y, hT, states, v_codes, v_exps, g_codes, g_exps, stream)
-    return y, hT, ScanSaved(v_codes, g_codes, v_exps, g_exps, states, lengths)
+    if checkpoint:
+        groups = (B, C, -(-L // WBMM_SEQ_GROUP))
+        vc, ve = torch.empty_like(v, dtype=torch.uint8), v.new_empty(groups, dtype=torch.uint8)
+        gc, ge = torch.empty_like(v, dtype=torch.uint8), v.new_empty(groups, dtype=torch.uint8)
+        kept = vc.data_ptr(), ve.data_ptr(), gc.data_ptr(), ge.data_ptr()
+        saved = ScanSaved(vc, gc, ve, ge, states, lengths)
+    else:
+        kept = None, None, None, None
+        saved = ScanSaved(v, g, None, None, states, lengths)
+    _check(_lib.wbmm_scan_forward(*inputs, y.data_ptr(), hT.data_ptr(), states.data_ptr(), *kept,
+                                  B, C, L, _dt(v), _stream(stream, v)))
+    return y, hT, saved
 
 
 def scan_backward(saved, dY, dhT=None, stream=None):
     """dv, dg and dh0 [B, C] fp32 from scan_forward_train's `saved`."""
-    if saved.v.numel() != dY.numel() or saved.v.shape[:2] != dY.shape[:2]:
+    v, g, v_exps, g_exps, states, lengths = saved
+    if v.numel() != dY.numel() or v.shape[:2] != dY.shape[:2]:
         raise WbmmError(WBMM_ERR_INVALID_ARG, "dY is %s, the forward call's maps were %s"
-                        % (tuple(dY.shape), tuple(saved.v.shape)))
+                        % (tuple(dY.shape), tuple(v.shape)))
+    B, C, L = _seq_shape(dY)
+    plain = v_exps is None
+    if not _all(dY.dtype if plain else torch.uint8, B * C * L, dY.get_device(), v, g):
+        _need("v", v, B * C * L, dY, None if plain else torch.uint8)
+        _need("g", g, B * C * L, dY, None if plain else torch.uint8)
+    _need_seq(dY, B, C, L, dhT, None, lengths, states, (), () if plain else (v_exps, g_exps))
     dv, dg = torch.empty_like(dY), torch.empty_like(dY)
-    dh0 = dY.new_empty(dY.shape[:2], dtype=torch.float32)
-    if saved.v_exps is None:
-        wbmm_scan_backward(saved.v, saved.g, saved.states, saved.lengths, dY, dhT, dv, dg, dh0,
-                           stream)
+    dh0 = dY.new_empty((B, C), dtype=torch.float32)
+    outputs = dv.data_ptr(), dg.data_ptr(), dh0.data_ptr(), B, C, L, _dt(dY), _stream(stream, dY)
+    if plain:
+        _check(_lib.wbmm_scan_backward(*_ptrs(v, g, states, lengths, dY, dhT), *outputs))
     else:
-        wbmm_scan_backward_checkpoint(saved.v, saved.v_exps, saved.g, saved.g_exps, saved.states,
-                                      saved.lengths, dY, dhT, dv, dg, dh0, stream)
+        _check(_lib.wbmm_scan_backward_checkpoint(
+            *_ptrs(v, v_exps, g, g_exps, states, lengths, dY, dhT), *outputs))
     return dv, dg, dh0
 
 
 def scan_step(v, g, h, stream=None):
     """One position for every row: y [B, C] and the next state [B, C] fp32."""
+    B, C, L = _seq_shape(v)
+    if L != 1:
+        raise ValueError("a step takes one position: [B, C]")
+    if not (_all(v.dtype, B * C, v.get_device(), g)
+            and _all(torch.float32, B * C, v.get_device(), h)):
+        _need("g", g, B * C, v)
+        _need("h", h, B * C, v, torch.float32)
+    pv, pg, ph = _ptrs(v, g, h)
     y, h_next = torch.empty_like(v), torch.empty_like(h)
-    wbmm_scan_step(v, g, h, y, h_next, stream)
+    _check(_lib.wbmm_scan_step(pv, pg, ph, y.data_ptr(), h_next.data_ptr(), B, C, _dt(v),
+                               _stream(stream, v)))
     return y, h_next
