@@ -6,8 +6,13 @@
 // Bands (the w image rows of one window row of a plane) follow each other in
 // the map, and a band's windows follow each other in the codes, so both
 // directions move whole bands with contiguous accesses and permute within a
-// band in shared memory: a block takes the next few bands, one thread a window
-// row.  Bound by memory: 3 bytes an element in bf16 and 5 in fp32.
+// band in shared memory: a block takes the next bands, at most 512 window rows,
+// a thread some of the rows.  The bytes are 3 an element in bf16 and 5 in fp32;
+// what bounds the kernels is the issue of instructions (0.7 of the slots, ncu),
+// 19 and 16 an element at w = 14.  128 x 256 bf16 maps of 28 x 28 in windows of
+// 14: stored in 19.5 us (61% of the measured copy rate), restored in 18.0 us
+// (66%).  4 rows a thread in 128 threads store faster than 2 in 256 (22.0 us) or
+// 8 in 128 (25.6 us), and restore slower (19.6 us), hence the two block sizes.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -97,8 +102,10 @@ __global__ void ckpt_restore_kernel(const uint8_t* __restrict__ codes,
 }
 
 // ------------------------------------------------------------ block kernels
-constexpr int kBandThreads = 256;
-constexpr int kBandRows = 2;            // window rows a thread, at most (WS > 0)
+constexpr int kStoreThreads = 128;
+constexpr int kRestoreThreads = 256;
+constexpr int kBandRows = 512;          // window rows a block, at most (WS > 0)
+constexpr int kStoreRows = kBandRows / kStoreThreads;
 constexpr int kBandElems = 8192;        // elements of a block's bands, at most
 
 struct BandArgs {
@@ -254,7 +261,7 @@ __device__ __forceinline__ void restore_row(T* e, const uint8_t* c, float st)
 // WS: the window size, 2 to 16 or 28 as the tensor-core kernels compile for,
 // or 0 for any other (w as given).
 template <typename T, int WS>
-__global__ void __launch_bounds__(kBandThreads)
+__global__ void __launch_bounds__(kStoreThreads)
     ckpt_store_bands_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes,
                             uint8_t* __restrict__ exps, const BandArgs P)
 {
@@ -270,16 +277,16 @@ __global__ void __launch_bounds__(kBandThreads)
     uint8_t* cds = img + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
     uint32_t* top = reinterpret_cast<uint32_t*>(cds + (P.nb * bn + 15) / 16 * 16);
     unsigned* place = reinterpret_cast<unsigned*>(top + P.nb * P.nw);
-    for (int k = tid; k < nb; k += kBandThreads)
+    for (int k = tid; k < nb; k += kStoreThreads)
         place[k] = band_place(P, f0 + k);
-    for (int k = tid; k < windows; k += kBandThreads)
+    for (int k = tid; k < windows; k += kStoreThreads)
         top[k] = 0u;
     grid_dep_wait();
     grid_dep_launch();
     const T* src = x + (long long)f0 * bn;
     const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
     const int bytes = nb * bn * (int)sizeof(T);
-    for (int lo = 16 * tid - off; lo < bytes; lo += 16 * kBandThreads) {
+    for (int lo = 16 * tid - off; lo < bytes; lo += 16 * kStoreThreads) {
         const uint8_t* from = reinterpret_cast<const uint8_t*>(src) + lo;
         if (lo >= 0 && lo + 16 <= bytes) {
             cp_async_16z(smem_u32(img + off + lo), from, 16u);
@@ -295,11 +302,11 @@ __global__ void __launch_bounds__(kBandThreads)
     const T* map = reinterpret_cast<const T*>(img + off);
     if constexpr (WS > 0) {
         // each thread's window rows stay in registers between the two passes
-        RowVals<T, WS> val[kBandRows];
-        int win[kBandRows], at[kBandRows];
+        RowVals<T, WS> val[kStoreRows];
+        int win[kStoreRows], at[kStoreRows];
 #pragma unroll
-        for (int m = 0; m < kBandRows; ++m) {
-            const int k = tid + m * kBandThreads;
+        for (int m = 0; m < kStoreRows; ++m) {
+            const int k = tid + m * kStoreThreads;
             if (k < rows) {
                 const WinRow q(P, k);
                 win[m] = q.band * P.nw + q.j;
@@ -310,8 +317,8 @@ __global__ void __launch_bounds__(kBandThreads)
         }
         __syncthreads();
 #pragma unroll
-        for (int m = 0; m < kBandRows; ++m) {
-            if (tid + m * kBandThreads < rows) {
+        for (int m = 0; m < kStoreRows; ++m) {
+            if (tid + m * kStoreThreads < rows) {
                 const uint32_t ex = group_exp(top[win[m]]);
                 if (ex >= kExpTop)
                     val[m].fix(ex);
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(kBandThreads)
             }
         }
     } else {
-        for (int k = tid; k < rows; k += kBandThreads) {
+        for (int k = tid; k < rows; k += kStoreThreads) {
             const WinRow q(P, k);
             const T* e = map + q.band * bn + q.r * P.W + q.j * w;
             uint32_t m = 0;
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kBandThreads)
             atomicMax(&top[q.band * P.nw + q.j], m);
         }
         __syncthreads();
-        for (int k = tid; k < rows; k += kBandThreads) {
+        for (int k = tid; k < rows; k += kStoreThreads) {
             const WinRow q(P, k);
             const T* e = map + q.band * bn + q.r * P.W + q.j * w;
             const uint32_t ex = group_exp(top[q.band * P.nw + q.j]);
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(kBandThreads)
         }
     }
     __syncthreads();
-    for (int k = tid; k < nb * P.units; k += kBandThreads) {
+    for (int k = tid; k < nb * P.units; k += kStoreThreads) {
         const int band = fast_div(k, P.div_units);
         const int at = (k - band * P.units) * P.unit;
         uint8_t* out = codes + (long long)place[band] * bn + at;
@@ -355,14 +362,14 @@ __global__ void __launch_bounds__(kBandThreads)
         else
             *out = *in;
     }
-    for (int k = tid; k < windows; k += kBandThreads) {
+    for (int k = tid; k < windows; k += kStoreThreads) {
         const int band = fast_div(k, P.div_nw);
         exps[(long long)place[band] * P.nw + (k - band * P.nw)] = (uint8_t)group_exp(top[k]);
     }
 }
 
 template <typename T, int WS>
-__global__ void __launch_bounds__(kBandThreads)
+__global__ void __launch_bounds__(kRestoreThreads)
     ckpt_restore_bands_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps,
                               T* __restrict__ x, const BandArgs P)
 {
@@ -376,12 +383,12 @@ __global__ void __launch_bounds__(kBandThreads)
     uint8_t* cds = img + (P.nb * bn * (int)sizeof(T) + 31) / 16 * 16;
     float* step = reinterpret_cast<float*>(cds + (P.nb * bn + 15) / 16 * 16);
     unsigned* place = reinterpret_cast<unsigned*>(step + P.nb * P.nw);
-    for (int k = tid; k < nb; k += kBandThreads)
+    for (int k = tid; k < nb; k += kRestoreThreads)
         place[k] = band_place(P, f0 + k);
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    for (int k = tid; k < nb * P.units; k += kBandThreads) {
+    for (int k = tid; k < nb * P.units; k += kRestoreThreads) {
         const int band = fast_div(k, P.div_units);
         const int at = (k - band * P.units) * P.unit;
         const uint8_t* in = codes + (long long)place[band] * bn + at;
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kBandThreads)
         else
             *to = *in;
     }
-    for (int k = tid; k < windows; k += kBandThreads) {
+    for (int k = tid; k < windows; k += kRestoreThreads) {
         const int band = fast_div(k, P.div_nw);
         step[k] = step_of(exps[(long long)place[band] * P.nw + (k - band * P.nw)]);
     }
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(kBandThreads)
     T* dst = x + (long long)f0 * bn;
     const int off = (int)(reinterpret_cast<uintptr_t>(dst) & 15);
     T* map = reinterpret_cast<T*>(img + off);
-    for (int k = tid; k < rows; k += kBandThreads) {
+    for (int k = tid; k < rows; k += kRestoreThreads) {
         const WinRow q(P, k);
         T* e = map + q.band * bn + q.r * P.W + q.j * w;
         const float st = step[q.band * P.nw + q.j];
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(kBandThreads)
     }
     __syncthreads();
     const int bytes = nb * bn * (int)sizeof(T);
-    for (int lo = 16 * tid - off; lo < bytes; lo += 16 * kBandThreads) {
+    for (int lo = 16 * tid - off; lo < bytes; lo += 16 * kRestoreThreads) {
         uint8_t* to = reinterpret_cast<uint8_t*>(dst) + lo;
         const uint8_t* from = img + off + lo;
         if (lo >= 0 && lo + 16 <= bytes) {
@@ -442,10 +449,10 @@ bool band_args(const Geom& g, size_t sz, int num_sms, BandArgs* P, size_t* smem)
         return false;
     P->bands = (unsigned)(g.bands * g.C);
     const int rows = g.nw * g.w;
-    // two window rows a thread, one where that would leave SMs without blocks
-    long long nb = kBandThreads * kBandRows / rows;
+    // fewer rows a block where that leaves SMs without blocks
+    long long nb = kBandRows / rows;
     if (P->bands < nb * 4 * num_sms)
-        nb = kBandThreads / rows;
+        nb = kBandRows / 2 / rows;
     nb = nb < 1 ? 1 : nb > kBandElems / bn ? kBandElems / bn : nb;
     P->nb = (int)nb;
     P->div_row = ceil_recip(rows);
@@ -467,11 +474,11 @@ auto pick_kernel(int w)
 }
 
 template <template <typename, int> class KernelT, typename T, typename... Args>
-cudaError_t band_launch(const BandArgs& P, size_t smem, const Launch& L, Args... args)
+cudaError_t band_launch(const BandArgs& P, int threads, size_t smem, const Launch& L, Args... args)
 {
-    const dim3 grid((P.bands + P.nb - 1) / P.nb), block(kBandThreads);
+    const dim3 grid((P.bands + P.nb - 1) / P.nb), block(threads);
     // the compiled sizes hold a block's window rows in registers
-    const bool fits = P.nb * P.nw * P.w <= kBandThreads * kBandRows;
+    const bool fits = P.nb * P.nw * P.w <= kBandRows;
     return launch_pdl(!fits        ? KernelT<T, 0>::get()
                       : P.w == 28 ? KernelT<T, 28>::get()
                                   : pick_kernel<KernelT, T, 16>(P.w),
@@ -506,9 +513,9 @@ cudaError_t checkpoint_launch(const Geom& g, bool is_bf16, const void* x, uint8_
     const dim3 grid(warp_grid(nwin * g.C, L)), block(128);
     if (band_args(g, is_bf16 ? 2 : 4, L.num_sms, &P, &smem))
         e = is_bf16 ? band_launch<StoreKernel, __nv_bfloat16>(
-                          P, smem, L, static_cast<const __nv_bfloat16*>(x), codes, exps)
-                    : band_launch<StoreKernel, float>(P, smem, L, static_cast<const float*>(x), codes,
-                                                      exps);
+                          P, kStoreThreads, smem, L, static_cast<const __nv_bfloat16*>(x), codes, exps)
+                    : band_launch<StoreKernel, float>(P, kStoreThreads, smem, L,
+                                                      static_cast<const float*>(x), codes, exps);
     else
         e = is_bf16 ? launch_pdl(ckpt_store_kernel<__nv_bfloat16>, grid, block, 0, L.stream,
                              static_cast<const __nv_bfloat16*>(x), codes, exps, g.C, g.H, g.W, g.w,
@@ -531,9 +538,9 @@ cudaError_t checkpoint_restore_launch(const Geom& g, bool is_bf16, const uint8_t
     const long long nwin = g.bands * g.nw;
     const dim3 grid(warp_grid(nwin * g.C, L)), block(128);
     if (band_args(g, is_bf16 ? 2 : 4, L.num_sms, &P, &smem))
-        e = is_bf16 ? band_launch<RestoreKernel, __nv_bfloat16>(P, smem, L, codes, exps,
+        e = is_bf16 ? band_launch<RestoreKernel, __nv_bfloat16>(P, kRestoreThreads, smem, L, codes, exps,
                                                                 static_cast<__nv_bfloat16*>(x))
-                    : band_launch<RestoreKernel, float>(P, smem, L, codes, exps,
+                    : band_launch<RestoreKernel, float>(P, kRestoreThreads, smem, L, codes, exps,
                                                         static_cast<float*>(x));
     else
         e = is_bf16 ? launch_pdl(ckpt_restore_kernel<__nv_bfloat16>, grid, block, 0, L.stream, codes,
