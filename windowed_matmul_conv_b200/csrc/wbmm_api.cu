@@ -217,9 +217,11 @@ wbmm_status backward_run(const Geom& g, const void* x, const unsigned char* code
     }
     // a checkpoint call takes its workspace as it is: the counters that the
     // launch uses are cleared here, ahead of the two kernels
-    if (tc_dt && clear && tc_dt_splits_channels(g, Lt.num_sms) &&
-        cudaMemsetAsync(workspace, 0, (size_t)g.C * 4, L.stream) != cudaSuccess)
-        return WBMM_ERR_CUDA;
+    if (tc_dt && clear && tc_dt_splits_channels(g, Lt.num_sms)) {
+        st = from_cuda(tc_dt_clear_launch(g, static_cast<float*>(workspace), L));
+        if (st != WBMM_OK)
+            return st;
+    }
     if (dX) {
         if (dt == WBMM_BF16 && tc_toep_supported(g)) {
             st = from_cuda(tc_toep_launch(g, kTableFlip, dY, T, dX, Lx));

@@ -97,6 +97,10 @@ cudaError_t tc_dt_launch(const Geom& g, const void* x, const void* dy, float* wo
 // arrivals in the workspace.
 bool tc_dt_splits_channels(const Geom& g, int num_sms);
 
+// Zeroes the workspace's counters of the call's channels, ahead of a launch on
+// a workspace whose content is unknown.
+cudaError_t tc_dt_clear_launch(const Geom& g, float* workspace, const Launch& L);
+
 // The same with x as an 8-bit checkpoint (a channel's codes a multiple of 16
 // bytes); equal, bit for bit, to tc_dt_launch on the restored map.
 bool tc_dt_codes_supported(const Geom& g);

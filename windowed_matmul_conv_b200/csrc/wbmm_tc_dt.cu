@@ -622,6 +622,16 @@ __global__ void __launch_bounds__(kDtThreads, 1) wbmm_tc_dt_kernel(const __grid_
         grid_dep_wait();
 }
 
+// Zeroes the arrival counters of a workspace whose content is unknown.
+__global__ void dt_clear_kernel(unsigned int* counters, int n)
+{
+    grid_dep_wait();
+    grid_dep_launch();
+    const int k = blockIdx.x * blockDim.x + threadIdx.x;
+    if (k < n)
+        counters[k] = 0u;
+}
+
 // ------------------------------------------------------------------ host
 namespace {
 
@@ -812,6 +822,16 @@ long long tc_dt_workspace_floats(const Geom& g)
 bool tc_dt_splits_channels(const Geom& g, int num_sms)
 {
     return dt_split(g, num_sms).unit == 1;
+}
+
+cudaError_t tc_dt_clear_launch(const Geom& g, float* workspace, const Launch& L)
+{
+    const cudaError_t e = launch_pdl(dt_clear_kernel, dim3((g.C + 255) / 256), dim3(256), 0, L.stream,
+                                     reinterpret_cast<unsigned int*>(workspace), g.C);
+    if (e != cudaSuccess)
+        return e;
+    note_launches(1);
+    return cudaGetLastError();
 }
 
 bool tc_dt_codes_supported(const Geom& g)
