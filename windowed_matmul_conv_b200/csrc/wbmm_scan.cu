@@ -19,10 +19,12 @@
 // where f (3e-35) is zero for every purpose and e f is 1.
 //
 // The bytes of a call (6 an element forward, 10 backward, in bf16) take the
-// memory 0.15 ns an element; the arithmetic is about 13 and 22 instructions an
-// element, half to two thirds of the issue slots in that time, so the code
-// around it is kept short: paired fp32 instructions (f32x2), one test a tile
-// for a partial tile, states and exponent bytes fetched for 32 tiles at once.
+// memory 0.9 and 1.6 ps an element; the kernels issue 25 and 40 instructions an
+// element (ncu; 44 and 45 with 8-bit forms), two thirds of the issue slots, and
+// reach 87% and 90% of the measured copy rate (27.5 and 44.0 us on 8192 rows of
+// 3136; 74% and 71% with 8-bit forms, 42.9 and 44.7 us).  So the code around the
+// arithmetic is kept short: paired fp32 instructions (f32x2), one test a tile for
+// a partial tile, states and exponent bytes fetched for 32 tiles at once.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -1486,11 +1488,12 @@ cudaError_t team_launch(const ScanArgs& A, bool backward, int ctas, const Launch
 }
 
 // Warps a row: one where that gives an SM 10 of them, else a team of 4, 8, 16
-// or 32 that does, so far as a row has that many tiles.  Measured, forward and
-// backward: 8192 rows of 3136 positions 28 and 43 us with a warp each, 39 and
-// 64 us with teams of 4; 768 rows of 50176 72 and 100 us, 57 and 78 us with
-// teams of 4, 78 and 104 us with teams of 8; 128 rows of 65536 31 and 51 us
-// with teams of 4, 24 and 37 us with 16, 23 and 43 us with 32.
+// or 32 that does, so far as a row has tiles for two each.  Measured, forward
+// and backward: 8192 rows of 3136 positions 28 and 43 us with a warp each, 39
+// and 64 us with teams of 4; 2048 rows of 4096 12 and 22 us, 12 and 20 us; 768
+// rows of 50176 81 and 128 us with a warp each, 43 and 79 us with teams of 4, 54
+// and 95 us with teams of 8; 128 rows of 65536 25 and 33 us with teams of 8, 20
+// and 24 us with 16, 22 and 28 us with 32.
 int team_for(long long rows, int L, int num_sms)
 {
     const long long tiles = ((long long)L + kScanTile - 1) / kScanTile;

@@ -194,6 +194,9 @@ struct DtWalker {
 // codes (one bulk copy); the producer warp keeps the exponent bytes of the
 // next tile in registers and leaves a tile's steps in its slot; the transform
 // restores the values, which bf16 holds exactly, on their way to the operand.
+// The x half of a tile's raw bytes halves; the time stays (B128 C256 28x28
+// w = 14, both gradients: 45.9 us against 44.2 from the bf16 map), since the
+// transform and the reductions of G bound the kernel, not the loads.
 template <int WS, bool CODES>
 __global__ void __launch_bounds__(kDtThreads, 1) wbmm_tc_dt_kernel(const __grid_constant__ TcDtParams P)
 {
