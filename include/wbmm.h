@@ -298,7 +298,9 @@ WBMM_API wbmm_status wbmm_backward_checkpoint(const unsigned char *codes,
  *     checkpoints of v and g as sequences, positions behind a sequence's end
  *     taken as zero.
  * The state, the gates and all sums are fp32 for both dtypes; y is rounded
- * once.  Results are bit-identical from run to run.
+ * once.  Results are bit-identical from run to run on a device (the split of
+ * few long rows depends on its SM count).  A state that has overflowed stays
+ * infinite or becomes NaN: distant steps are composed before they meet it.
  * Errors: INVALID_ARG (null pointer, B, C or L <= 0, overlap), DTYPE,
  * ALIGNMENT, UNSUPPORTED (B*C >= 2^31 or L >= 2^31 - 65536), CUDA.
  */

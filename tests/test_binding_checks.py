@@ -154,3 +154,8 @@ def test_recurrence_buffers(wb):
         wb.wbmm_scan_step(x, x, h, x, h)
     with pytest.raises(ValueError):
         wb.scan_forward(x[0, 0], x[0, 0])
+    # more positions than the C ABI's int holds (an expanded view: no memory)
+    huge = torch.zeros(1, dtype=BF).expand(1, 1, 1 << 32)
+    with pytest.raises(wb.WbmmError) as e:
+        wb.wbmm_scan_forward(huge, huge, None, None, huge, *[None] * 6)
+    assert e.value.status == 5

@@ -92,7 +92,8 @@ for _f in ("wbmm_forward", "wbmm_backward", "wbmm_backward_dt_static", "wbmm_cac
     getattr(_lib, _f).restype = _i
 
 
-WBMM_ERR_INVALID_ARG, WBMM_ERR_DTYPE = 1, 3
+WBMM_ERR_INVALID_ARG, WBMM_ERR_DTYPE, WBMM_ERR_UNSUPPORTED = 1, 3, 5
+_INT_MAX = 0x7fffffff
 
 
 class WbmmError(RuntimeError):
@@ -202,13 +203,13 @@ def _windows(B, C, H, W, w):
 
 def _seq_shape(v):
     shape = v.shape
-    if len(shape) == 3:
-        return shape
-    if len(shape) == 2:
-        return shape[0], shape[1], 1
     if len(shape) < 2:
         raise ValueError("recurrence tensors must be [B, C, L], [B, C, H, W] or [B, C]")
-    return shape[0], shape[1], math.prod(shape[2:])
+    B, C = shape[0], shape[1]
+    L = shape[2] if len(shape) == 3 else math.prod(shape[2:])
+    if L > _INT_MAX or B > _INT_MAX or C > _INT_MAX:     # the C ABI's sizes are ints
+        raise WbmmError(WBMM_ERR_UNSUPPORTED, "sizes %s" % (tuple(shape),))
+    return B, C, L
 
 
 def _need_seq(ref, B, C, L, h0, hT, lengths, states, codes=(), exps=()):

@@ -460,7 +460,7 @@ struct BackSteps {
 // tile's ends are written element by element.  (fp32 rows go that way even
 // where they are aligned: a lane's 32 bytes would be two 16-byte accesses 32
 // bytes apart, each half of every sector; B32 C256 L1568 forward 40 us against
-// 34 us through the image.)
+// 31 us through the image.)
 
 __device__ __forceinline__ uint4 lds4(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
@@ -688,7 +688,7 @@ struct Stage {
     // four stages; three of the larger fp32 ones where a warp works alone
     // (more warps fit an SM: B32 C256 L1568 forward 32.0 us, 34.0 with four)
     // and where four would not fit (fp32 backward)
-    static constexpr int DEPTH = BYTES > (TEAM ? 3072 : 2048) ? 3 : 4;
+    static constexpr int DEPTH = BYTES > (TEAM ? 3000 : 2048) ? 3 : 4;
     // tiles a round: a team's warp takes two, whose arithmetic overlaps and
     // which share the round's barrier, where the ring holds two rounds (768
     // rows of 50176 forward 43.0 us, 57.5 with one)
@@ -741,9 +741,9 @@ struct Stream {
 
 // Where several warps take one row: a team of the 4 warps of a CTA, or of all
 // CTAs of a cluster.  In each round warp k of the team has the round's k-th
-// tile, publishes the tile's composed map in the shared memory of every CTA of
-// the team, and, after one barrier, applies the maps of the warps before its
-// own to the state that all of them carry from round to round.  Rounds
+// tile or pair of tiles, publishes its composed map in the shared memory of
+// every CTA of the team, and, after one barrier, applies the maps of the warps
+// before its own to the state that all of them carry from round to round.  Rounds
 // alternate between two slot arrays, so one barrier a round is enough: a warp
 // overwrites a slot only after the next barrier, which its readers have passed
 // by then.  A CTA's last remote access comes before the last barrier, so none
@@ -763,7 +763,7 @@ struct Team {
         if (ctas > 1)
             cluster_sync();     // every CTA of the cluster has started
     }
-    // A and H are the tile's, on every lane.
+    // A and H are the warp's map of the round, on every lane.
     __device__ __forceinline__ void publish(int buf, float A, float H, int lane)
     {
         if (ctas == 1) {
@@ -777,7 +777,7 @@ struct Team {
             cluster_sync();
         }
     }
-    // The state before this warp's tile, from the one before the round's
+    // The state before this warp's tiles, from the one before the round's
     // first (REV: behind its last); `s` becomes the one after the round.
     template <bool REV>
     __device__ __forceinline__ float join(int buf, float& s) const
