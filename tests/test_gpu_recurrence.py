@@ -373,3 +373,22 @@ def test_saved_of_another_shape_is_refused():
         wb.scan_forward(d["v"].reshape(-1)[1:41].view(1, 1, 40), d["g"].reshape(-1)[1:41].view(1, 1, 40))
     assert e.value.status == 4
     assert wb.wbmm_launch_count() == before
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(2, 3, 250), (2, 3, 257), (2, 3, 519), (2, 3, 1279), (2, 3, 1024), (1, 2, 9001)])
+def test_one_states_array_serves_both_backward_calls(shape, kind):
+    """The kept states are those before every 256th position, with 8-bit forms
+    or without, so that either forward call's serve the other's backward."""
+    d = make(*shape, kind, 121)
+    plain = wb.scan_forward_train(d["v"], d["g"], d["h0"])[2]
+    coded = wb.scan_forward_train(d["v"], d["g"], d["h0"], checkpoint=True)[2]
+    v, g, h0 = np64(d["v"]), np64(d["g"]), np64(d["h0"])
+    every = slice(0, shape[2], orc.TILE)
+    want, tol = orc.scan(v, g, h0)[1][:, :, every], bounds(v, g, kind, h0, None)["h"][:, :, every]
+    close(plain.states, want, tol, "states")
+    close(coded.states, want, tol, "states beside 8-bit forms")
+    for a, b in ((plain, coded), (coded, plain)):
+        for p, q in zip(wb.scan_backward(a, d["dY"], d["dhT"]),
+                        wb.scan_backward(a._replace(states=b.states), d["dY"], d["dhT"])):
+            assert torch.equal(p, q)
