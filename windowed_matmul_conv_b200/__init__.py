@@ -17,7 +17,10 @@ The convenience functions ``forward``, ``backward``, ``cache_matrices``,
 ``reparam_merge``, ``forward_cached``, ``dw3x3``, ``checkpoint``,
 ``checkpoint_restore``, ``backward_checkpoint``, ``scan_forward``,
 ``scan_forward_train``, ``scan_backward`` and ``scan_step`` allocate outputs
-with torch and call the entry points above.
+with torch and call the entry points above.  With ``stream`` they run as under
+``torch.cuda.stream(stream)``: outputs and workspaces come from that stream's
+memory, and another stream that uses the outputs waits for it first (and calls
+``record_stream`` on what it may free).
 """
 import ctypes
 import math
@@ -423,13 +426,26 @@ def wbmm_debug_set(what, value):
 
 # ------------------------------------------------------------ conveniences
 
+def _on(stream, ref, call, *args, **kw):
+    """A convenience call on a given stream.  What it allocates has to come from
+    that stream's memory: the current stream's may still be in use there, and a
+    workspace freed to it would be handed out while the kernels run."""
+    _p(ref), _stream(stream, ref)
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
 def forward(x, T, w, stream=None):
+    if stream is not None:
+        return _on(stream, x, forward, x, T, w)
     y = torch.empty_like(x)
-    wbmm_forward(x, T, y, w, stream)
+    wbmm_forward(x, T, y, w)
     return y
 
 
 def backward(x, T, dY, w, need_dx=True, need_dt=True, stream=None):
+    if stream is not None:
+        return _on(stream, dY, backward, x, T, dY, w, need_dx, need_dt)
     B, C, H, W = _map_shape(dY)
     dX = torch.empty_like(dY) if need_dx else None
     dT = torch.empty((C, (2 * w - 1) ** 2), dtype=torch.float32, device=dY.device) if need_dt else None
@@ -438,7 +454,7 @@ def backward(x, T, dY, w, need_dx=True, need_dt=True, stream=None):
         nbytes = wbmm_backward_workspace_bytes(B, C, H, W, w, dY.dtype)
         # zero-filled: the table gradient's arrival counters start at zero
         ws = torch.zeros(max(1, nbytes // 4), dtype=torch.float32, device=dY.device)
-    wbmm_backward(x, T, dY, dX, dT, ws, w, stream)
+    wbmm_backward(x, T, dY, dX, dT, ws, w)
     return dX, dT
 
 
@@ -455,26 +471,34 @@ def wbmm_reparam_merge(Tw, Tk, M, w, k, stream=None):
 def reparam_merge(Tw, Tk, w, k, stream=None):
     """Inference matrix [C, w*w, w*w] of a w-window branch (table Tw) plus a
     k-window branch (table Tk), k dividing w; feed it to forward_cached."""
+    if stream is not None:
+        return _on(stream, Tw, reparam_merge, Tw, Tk, w, k)
     M = torch.empty((Tw.shape[0], w * w, w * w), dtype=Tw.dtype, device=Tw.device)
-    wbmm_reparam_merge(Tw, Tk, M, w, k, stream)
+    wbmm_reparam_merge(Tw, Tk, M, w, k)
     return M
 
 
 def cache_matrices(T, w, stream=None):
+    if stream is not None:
+        return _on(stream, T, cache_matrices, T, w)
     M = torch.empty((T.shape[0], w * w, w * w), dtype=T.dtype, device=T.device)
-    wbmm_cache_matrices(T, M, w, stream)
+    wbmm_cache_matrices(T, M, w)
     return M
 
 
 def forward_cached(x, M, w, dw=None, stream=None):
+    if stream is not None:
+        return _on(stream, x, forward_cached, x, M, w, dw)
     out = torch.empty_like(x)
-    wbmm_forward_cached(x, M, dw, out, w, stream)
+    wbmm_forward_cached(x, M, dw, out, w)
     return out
 
 
 def dw3x3(y, K, stream=None):
+    if stream is not None:
+        return _on(stream, y, dw3x3, y, K)
     z = torch.empty_like(y)
-    wbmm_dw3x3(y, K, z, stream)
+    wbmm_dw3x3(y, K, z)
     return z
 
 
@@ -484,30 +508,36 @@ def dw3x3(y, K, stream=None):
 def checkpoint(x, w, stream=None):
     """8-bit form of a map: codes [C, B*nh*nw, w*w] and exponent bytes
     [C, B*nh*nw], one power-of-two step per window."""
+    if stream is not None:
+        return _on(stream, x, checkpoint, x, w)
     B, C, H, W = _map_shape(x)
     px, = _ptrs(x)
     n = _windows(B, C, H, W, w) // max(1, C)
     codes = x.new_empty((C, n, x.numel() // max(1, C * n)), dtype=torch.uint8)
     exps = x.new_empty((C, n), dtype=torch.uint8)
     _check(_lib.wbmm_checkpoint(px, codes.data_ptr(), exps.data_ptr(), B, C, H, W, int(w), _dt(x),
-                                _stream(stream, x)))
+                                _stream(None, x)))
     return codes, exps
 
 
 def checkpoint_restore(codes, exps, shape, w, dtype, stream=None):
     """The map of the given shape and dtype that checkpoint() stored."""
+    if stream is not None:
+        return _on(stream, codes, checkpoint_restore, codes, exps, shape, w, dtype)
     B, C, H, W = shape
     x = codes.new_empty(shape, dtype=dtype)
     _need("codes", codes, B * C * H * W, x, torch.uint8)
     _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
     pc, pe = _ptrs(codes, exps)
     _check(_lib.wbmm_checkpoint_restore(pc, pe, x.data_ptr(), B, C, H, W, int(w), _dt(x),
-                                        _stream(stream, x)))
+                                        _stream(None, x)))
     return x
 
 
 def backward_checkpoint(codes, exps, T, dY, w, need_dx=True, need_dt=True, stream=None):
     """backward() with the forward's input as checkpoint() keeps it."""
+    if stream is not None:
+        return _on(stream, dY, backward_checkpoint, codes, exps, T, dY, w, need_dx, need_dt)
     B, C, H, W = _map_shape(dY)
     dX = torch.empty_like(dY) if need_dx else None
     dT = dY.new_empty((C, (2 * w - 1) ** 2), dtype=torch.float32) if need_dt else None
@@ -515,7 +545,7 @@ def backward_checkpoint(codes, exps, T, dY, w, need_dx=True, need_dt=True, strea
     if need_dt:
         nbytes = wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dY.dtype)
         ws = dY.new_empty(nbytes, dtype=torch.uint8)
-    wbmm_backward_checkpoint(codes, exps, T, dY, dX, dT, ws, w, stream)
+    wbmm_backward_checkpoint(codes, exps, T, dY, dX, dT, ws, w)
     return dX, dT
 
 
@@ -545,16 +575,20 @@ def _scan_inputs(v, g, h0, lengths):
 
 def scan_forward(v, g, h0=None, lengths=None, stream=None):
     """y and the last state [B, C] fp32 of the gated recurrence over [B, C, L]."""
+    if stream is not None:
+        return _on(stream, v, scan_forward, v, g, h0, lengths)
     B, C, L, inputs = _scan_inputs(v, g, h0, lengths)
     y, hT = torch.empty_like(v), v.new_empty((B, C), dtype=torch.float32)
     _check(_lib.wbmm_scan_forward(*inputs, y.data_ptr(), hT.data_ptr(), None, None, None, None,
-                                  None, B, C, L, _dt(v), _stream(stream, v)))
+                                  None, B, C, L, _dt(v), _stream(None, v)))
     return y, hT
 
 
 def scan_forward_train(v, g, h0=None, lengths=None, checkpoint=False, stream=None):
     """scan_forward that also returns what scan_backward needs; with
     `checkpoint` v and g are kept in 8 bits."""
+    if stream is not None:
+        return _on(stream, v, scan_forward_train, v, g, h0, lengths, checkpoint)
     B, C, L, inputs = _scan_inputs(v, g, h0, lengths)
     y, hT = torch.empty_like(v), v.new_empty((B, C), dtype=torch.float32)
     states = v.new_empty((B, C, _scan_tiles(L)), dtype=torch.float32)
@@ -568,12 +602,14 @@ def scan_forward_train(v, g, h0=None, lengths=None, checkpoint=False, stream=Non
         kept = None, None, None, None
         saved = ScanSaved(v, g, None, None, states, lengths)
     _check(_lib.wbmm_scan_forward(*inputs, y.data_ptr(), hT.data_ptr(), states.data_ptr(), *kept,
-                                  B, C, L, _dt(v), _stream(stream, v)))
+                                  B, C, L, _dt(v), _stream(None, v)))
     return y, hT, saved
 
 
 def scan_backward(saved, dY, dhT=None, stream=None):
     """dv, dg and dh0 [B, C] fp32 from scan_forward_train's `saved`."""
+    if stream is not None:
+        return _on(stream, dY, scan_backward, saved, dY, dhT)
     v, g, v_exps, g_exps, states, lengths = saved
     if v.numel() != dY.numel() or v.shape[:2] != dY.shape[:2]:
         raise WbmmError(WBMM_ERR_INVALID_ARG, "dY is %s, the forward call's maps were %s"
@@ -586,7 +622,7 @@ def scan_backward(saved, dY, dhT=None, stream=None):
     _need_seq(dY, B, C, L, dhT, None, lengths, states, (), () if plain else (v_exps, g_exps))
     dv, dg = torch.empty_like(dY), torch.empty_like(dY)
     dh0 = dY.new_empty((B, C), dtype=torch.float32)
-    outputs = dv.data_ptr(), dg.data_ptr(), dh0.data_ptr(), B, C, L, _dt(dY), _stream(stream, dY)
+    outputs = dv.data_ptr(), dg.data_ptr(), dh0.data_ptr(), B, C, L, _dt(dY), _stream(None, dY)
     if plain:
         _check(_lib.wbmm_scan_backward(*_ptrs(v, g, states, lengths, dY, dhT), *outputs))
     else:
@@ -597,6 +633,8 @@ def scan_backward(saved, dY, dhT=None, stream=None):
 
 def scan_step(v, g, h, stream=None):
     """One position for every row: y [B, C] and the next state [B, C] fp32."""
+    if stream is not None:
+        return _on(stream, v, scan_step, v, g, h)
     B, C, L = _seq_shape(v)
     if L != 1:
         raise ValueError("a step takes one position: [B, C]")
@@ -607,5 +645,5 @@ def scan_step(v, g, h, stream=None):
     pv, pg, ph = _ptrs(v, g, h)
     y, h_next = torch.empty_like(v), torch.empty_like(h)
     _check(_lib.wbmm_scan_step(pv, pg, ph, y.data_ptr(), h_next.data_ptr(), B, C, _dt(v),
-                               _stream(stream, v)))
+                               _stream(None, v)))
     return y, h_next
