@@ -193,14 +193,24 @@ def _tsz(w):
     return (2 * int(w) - 1) ** 2
 
 
+def _ints(*sizes):
+    """Refuses sizes beyond the C ABI's ints, which ctypes would cut to 32 bits."""
+    for n in sizes:
+        if not -_INT_MAX <= n <= _INT_MAX:
+            raise WbmmError(WBMM_ERR_UNSUPPORTED, "sizes %s" % (sizes,))
+
+
 def _map_shape(x):
     if x.dim() != 4:
         raise ValueError("feature maps must be [B, C, H, W]")
+    if x.numel() > _INT_MAX:            # no size is larger than the product, but for empty maps
+        _ints(*x.shape)
     return x.shape
 
 
 def _windows(B, C, H, W, w):
     w = int(w)
+    _ints(w)
     return B * C * (H // w) * (W // w) if w > 0 else 0
 
 
@@ -210,8 +220,7 @@ def _seq_shape(v):
         raise ValueError("recurrence tensors must be [B, C, L], [B, C, H, W] or [B, C]")
     B, C = shape[0], shape[1]
     L = shape[2] if len(shape) == 3 else math.prod(shape[2:])
-    if L > _INT_MAX or B > _INT_MAX or C > _INT_MAX:     # the C ABI's sizes are ints
-        raise WbmmError(WBMM_ERR_UNSUPPORTED, "sizes %s" % (tuple(shape),))
+    _ints(B, C, L)
     return B, C, L
 
 
@@ -249,6 +258,7 @@ def wbmm_forward(x, T, y, w, stream=None):
 
 def wbmm_backward_workspace_bytes(B, C, H, W, w, dtype):
     dt = _dt(torch.empty(0, dtype=dtype))
+    _ints(B, C, H, W, int(w))
     return int(_lib.wbmm_backward_workspace_bytes(B, C, H, W, int(w), dt))
 
 
@@ -278,6 +288,7 @@ def wbmm_backward_dt_static(x, dY, dT, w, stream=None):
 def wbmm_cache_matrices(T, M, w, stream=None):
     """T: [C, (2w-1)^2]; M: [C, w*w, w*w]."""
     C = int(T.shape[0])
+    _ints(C)
     _need("T", T, C * _tsz(w), T)
     _need("M", M, C * int(w) ** 4, T)
     _check(_lib.wbmm_cache_matrices(_p(T), _p(M), C, int(w), _dt(T), _stream(stream, T)))
@@ -319,6 +330,7 @@ def wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, w, dtype):
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise TypeError("WBMM tensors must be bfloat16 or float32, got %s" % dtype)
+    _ints(B, C, H, W, int(w))
     return int(_lib.wbmm_backward_checkpoint_workspace_bytes(B, C, H, W, int(w), dt))
 
 
@@ -352,6 +364,7 @@ def wbmm_scan_forward(v, g, h0, lengths, y, hT, states, v_codes, v_exps, g_codes
 
 
 def wbmm_scan_states_bytes(B, C, L):
+    _ints(B, C, L)
     return int(_lib.wbmm_scan_states_bytes(int(B), int(C), int(L)))
 
 
@@ -461,6 +474,7 @@ def backward(x, T, dY, w, need_dx=True, need_dt=True, stream=None):
 def wbmm_reparam_merge(Tw, Tk, M, w, k, stream=None):
     """Tw: [C, (2w-1)^2]; Tk: [C, (2k-1)^2]; M: [C, w*w, w*w]."""
     C = int(Tw.shape[0])
+    _ints(C)
     _need("Tw", Tw, C * _tsz(w), Tw)
     _need("Tk", Tk, C * _tsz(k), Tw)
     _need("M", M, C * int(w) ** 4, Tw)
@@ -525,6 +539,7 @@ def checkpoint_restore(codes, exps, shape, w, dtype, stream=None):
     if stream is not None:
         return _on(stream, codes, checkpoint_restore, codes, exps, shape, w, dtype)
     B, C, H, W = shape
+    _ints(B, C, H, W)
     x = codes.new_empty(shape, dtype=dtype)
     _need("codes", codes, B * C * H * W, x, torch.uint8)
     _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
