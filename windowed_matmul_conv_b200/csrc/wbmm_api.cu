@@ -170,15 +170,14 @@ struct SeqSizes {
     bool supported(int L) const { return rows < (1ll << 31) && L <= 0x7fffffff - 65536; }
 };
 
-// True when an output overlaps an input or another output; `carry_in` and
-// `carry_out` (a state updated in place) may be one buffer.
-bool clash(const Span* in, int nin, const Span* out, int nout, const void* carry_in,
-           const void* carry_out)
+// True when an output overlaps an input or another output; in[state_in] and
+// out[state_out] (a state updated in place) may be one buffer.
+bool clash(const Span* in, int nin, const Span* out, int nout, int state_in, int state_out)
 {
     for (int o = 0; o < nout; ++o) {
         for (int i = 0; i < nin; ++i)
             if (overlap(in[i], out[o]) &&
-                !(in[i].p == carry_in && out[o].p == carry_out && carry_in == carry_out))
+                !(i == state_in && o == state_out && in[i].p == out[o].p))
                 return true;
         for (int q = 0; q < o; ++q)
             if (overlap(out[q], out[o]))
@@ -277,7 +276,7 @@ wbmm_status scan_backward_checked(ScanArgs A, const float* states, const int* le
                        {states, z.states},    {lengths, (size_t)B * 4}, {dY, z.map},
                        {dhT, z.state}};
     const Span out[] = {{dv, z.map}, {dg, z.map}, {dh0, z.state}};
-    if (clash(in, 10, out, 3, dhT, dh0))
+    if (clash(in, 10, out, 3, 9, 2))
         return WBMM_ERR_INVALID_ARG;
     Launch Ln;
     wbmm_status st = make_launch(stream, &Ln);
@@ -677,7 +676,7 @@ wbmm_status wbmm_scan_forward(const void* v, const void* g, const float* h0, con
     const Span out[] = {{y, z.map},          {hT, z.state},       {states, z.states},
                         {v_codes, z.codes},  {v_exps, z.exps},    {g_codes, z.codes},
                         {g_exps, z.exps}};
-    if (clash(in, 4, out, 7, h0, hT))
+    if (clash(in, 4, out, 7, 2, 1))
         return WBMM_ERR_INVALID_ARG;
     Launch Ln;
     wbmm_status st = make_launch(stream, &Ln);
@@ -741,7 +740,7 @@ wbmm_status wbmm_scan_step(const void* v, const void* g, const float* h, void* y
         return WBMM_ERR_UNSUPPORTED;
     const Span in[] = {{v, z.map}, {g, z.map}, {h, z.state}};
     const Span out[] = {{y, z.map}, {h_next, z.state}};
-    if (clash(in, 3, out, 2, h, h_next))
+    if (clash(in, 3, out, 2, 2, 1))
         return WBMM_ERR_INVALID_ARG;
     Launch L;
     wbmm_status st = make_launch(stream, &L);
