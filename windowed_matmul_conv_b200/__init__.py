@@ -178,11 +178,10 @@ def _all(dtype, numel, device, *tensors):
 def _ptrs(*tensors):
     """Addresses of tensors that are on one device (checked): CUDA, contiguous."""
     out = []
-    cuda = tensors[0].is_cuda
     for t in tensors:
         if t is None:
             out.append(None)
-        elif cuda and t.is_contiguous():
+        elif t.is_cuda and t.is_contiguous():
             out.append(t.data_ptr())
         else:
             raise ValueError("WBMM tensors must be contiguous CUDA tensors")
