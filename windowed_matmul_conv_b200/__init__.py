@@ -528,7 +528,9 @@ def checkpoint(x, w, stream=None):
     n = _windows(B, C, H, W, w) // max(1, C)
     codes = x.new_empty((C, n, x.numel() // max(1, C * n)), dtype=torch.uint8)
     exps = x.new_empty((C, n), dtype=torch.uint8)
-    _check(_lib.wbmm_checkpoint(px, codes.data_ptr(), exps.data_ptr(), B, C, H, W, int(w), _dt(x),
+    # a map without a whole window has no groups to point to; its shape is refused
+    pc, pe = (codes.data_ptr(), exps.data_ptr()) if n else (px, px)
+    _check(_lib.wbmm_checkpoint(px, pc, pe, B, C, H, W, int(w), _dt(x),
                                 _stream(None, x)))
     return codes, exps
 
