@@ -129,14 +129,6 @@ __device__ __forceinline__ void cp_async_4(uint32_t smem_dst, const void *gsrc)
                  : "memory");
 }
 
-// The same reading src_bytes (0 to 4) and zero-filling the rest.
-__device__ __forceinline__ void cp_async_4z(uint32_t smem_dst, const void *gsrc, uint32_t src_bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_dst), "l"(gsrc),
-                 "r"(src_bytes)
-                 : "memory");
-}
-
 // Global -> shared copy of 8 bytes, both addresses 8-byte aligned.
 __device__ __forceinline__ void cp_async_8(uint32_t smem_dst, const void *gsrc)
 {
