@@ -219,7 +219,9 @@ WBMM_API wbmm_status wbmm_backward_dt_static(const void *x, const void *dY, floa
  *   exponent byte = e + 127                            (1..248)
  * and stands for (code - 128) * 2^e, which bf16 and fp32 hold exactly, so
  * storing a restored map again gives the same bytes.  |restored - x| is at
- * most half a step, a/127 (a above 2^127 * 1.99 saturates to 127 steps).  A
+ * most half a step, which is at most a/127 where e is not at an end of its
+ * range: with e = -126 (a below 2^-120) half a step is 2^-127, and with
+ * e = 121 values beyond 127 steps (2^127 * 1.98) saturate there.  A
  * group that holds a NaN or an infinity has exponent byte 255 and codes 128
  * and restores to NaN throughout, so an overflow in the forward pass is not
  * hidden from the backward pass.
@@ -296,9 +298,15 @@ WBMM_API wbmm_status wbmm_backward_checkpoint(const unsigned char *codes,
  *     recomputes the others.  Entries behind a sequence's end are not written.
  *   v_codes, v_exps, g_codes, g_exps: all four or none; receive 8-bit
  *     checkpoints of v and g as sequences, positions behind a sequence's end
- *     taken as zero.
+ *     taken as zero.  A restored gate is off by at most half its group's step,
+ *     and f and 1 - f with it by a factor of at most exp(half a step): 3% in
+ *     a group whose largest |g| is 4 to 8, 6% where it is 8 to 16.  One gate
+ *     far beyond the others makes their steps coarse, and an infinite one the
+ *     whole group NaN: hold the gates within the range that matters, say
+ *     -16 to 16, before a call that keeps them.
  * The state, the gates and all sums are fp32 for both dtypes; y is rounded
- * once.  Results are bit-identical from run to run on a device (the split of
+ * once.  A gate below about -79.5, an infinite one too, counts as that: 3e-35
+ * of the state before it remains.  Results are bit-identical from run to run on a device (the split of
  * few long rows depends on its SM count).  A state that has overflowed stays
  * infinite or becomes NaN: distant steps are composed before they meet it.
  * Errors: INVALID_ARG (null pointer, B, C or L <= 0, overlap), DTYPE,
@@ -331,7 +339,8 @@ WBMM_API wbmm_status wbmm_scan_backward(const void *v, const void *g, const floa
 
 /*
  * The same with v and g taken from the 8-bit checkpoints that the forward
- * call wrote; the states at every 256th position are the forward's own.
+ * call wrote: the gradients of the recurrence on the restored inputs, whose
+ * states start again at every 256th position from the forward's own.
  */
 WBMM_API wbmm_status wbmm_scan_backward_checkpoint(
     const unsigned char *v_codes, const unsigned char *v_exps, const unsigned char *g_codes,

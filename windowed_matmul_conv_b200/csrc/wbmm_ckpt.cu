@@ -8,11 +8,13 @@
 // directions move whole bands with contiguous accesses and permute within a
 // band in shared memory: a block takes the next bands, at most 512 window rows,
 // a thread some of the rows.  The bytes are 3 an element in bf16 and 5 in fp32;
-// what bounds the kernels is the issue of instructions (0.7 of the slots, ncu),
-// 19 and 16 an element at w = 14.  128 x 256 bf16 maps of 28 x 28 in windows of
-// 14: stored in 19.5 us (61% of the measured copy rate), restored in 18.0 us
-// (66%).  4 rows a thread in 128 threads store faster than 2 in 256 (22.0 us) or
-// 8 in 128 (25.6 us), and restore slower (19.6 us), hence the two block sizes.
+// the instructions, 16 an element in both directions at w = 14 and 28 and 25 at
+// w = 7 (bf16, ncu), take 67 to 82% of the issue slots, and the barriers between
+// a block's three passes are among its warps' longest waits.  128 x 256 maps of
+// 28 x 28 in windows of 14: bf16 stored in 19.4 us (62% of the measured copy
+// rate), restored in 17.9 us (67%); fp32 28.8 us (69%) and 28.2 us (71%).  4 rows a
+// thread in 128 threads store faster than 2 in 256 (22.0 us) or 8 in 128 (25.6
+// us), and restore slower (19.6 us), hence the two block sizes.
 #include <cuda_bf16.h>
 
 #include <type_traits>

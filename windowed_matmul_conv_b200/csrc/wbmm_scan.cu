@@ -15,16 +15,18 @@
 // reversed recurrence of c_t = f_t (dy_t + c_{t+1}).
 //
 // 1 - f is e f with e = exp(-g), not a difference, so that it keeps its
-// relative accuracy where f is close to 1; -g is held at about 79.6 at most,
-// where f (3e-35) is zero for every purpose and e f is 1.
+// relative accuracy where f is close to 1; -g is held at about 79.6 at most, so
+// that e stays finite: e f is 1 there, and 3e-35 of the state before remains.
 //
 // The bytes of a call (6 an element forward, 10 backward, in bf16) take the
 // memory 0.9 and 1.6 ps an element; the kernels issue 25 and 40 instructions an
-// element (ncu; 44 and 45 with 8-bit forms), two thirds of the issue slots, and
-// reach 87% and 90% of the measured copy rate (27.5 and 44.0 us on 8192 rows of
-// 3136; 74% and 71% with 8-bit forms, 42.9 and 44.7 us).  So the code around the
-// arithmetic is kept short: paired fp32 instructions (f32x2), one test a tile for
-// a partial tile, states and exponent bytes fetched for 32 tiles at once.
+// element (ncu; 44 and 45 with 8-bit forms) and reach 87% and 90% of the measured
+// copy rate (27.5 and 44.0 us on 8192 rows of 3136; 75% and 72% with 8-bit forms,
+// 42.8 and 44.5 us).  Two thirds of the issue slots are taken, with a third of the
+// warps resident: both the instructions and the latency that so few warps hide
+// are in the way.  So the code around the arithmetic is kept short: paired fp32
+// instructions (f32x2), one test a tile for a partial tile, states and exponent
+// bytes fetched for 32 tiles at once.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -1487,13 +1489,20 @@ cudaError_t team_launch(const ScanArgs& A, bool backward, int ctas, const Launch
                                    A));
 }
 
-// Warps a row: one where that gives an SM 10 of them, else a team of 4, 8, 16
-// or 32 that does, so far as a row has tiles for two each.  Measured, forward
-// and backward: 8192 rows of 3136 positions 28 and 43 us with a warp each, 39
-// and 64 us with teams of 4; 2048 rows of 4096 12 and 22 us, 12 and 20 us; 768
-// rows of 50176 81 and 128 us with a warp each, 43 and 79 us with teams of 4, 54
-// and 95 us with teams of 8; 128 rows of 65536 25 and 33 us with teams of 8, 20
-// and 24 us with 16, 22 and 28 us with 32.
+// Warps a row: one where that gives an SM 10 of them, else a team of 4 for rows
+// of 2 tiles or more, of 8, 16 and 32 while that gives an SM fewer than 10 and a
+// row has two tiles for each warp of the team that is doubled (so one for each
+// of the doubled one).  Measured, forward and backward, bf16: 8192 rows of 3136
+// positions 28 and 43 us with a warp each, 39 and 64 us with teams of 4; 1600
+// rows of 4096 10.0 and 15.6 us, 9.7 and 16.4 us; of 16384 31.7 and 49.8 us, 27.6
+// and 46.0 us; 768 rows of 50176 81 and 128 us with a warp each, 43 and 79 us with
+// teams of 4, 54 and 95 us with teams of 8; 128 rows of 65536 25 and 33 us with
+// teams of 8, 20 and 24 us with 16, 22 and 28 us with 32.  Near the rule's edges:
+// 64 rows of 4096 2.8 and 3.6 us with teams of 4, 3.0 and 3.3 with 8, 3.0 and 3.6
+// with 16 (taken), 6.4 and 9.7 with a warp each; 64 rows of 2048 2.1 and 2.5 us
+// with 4, 2.8 and 3.3 with 8 (taken), 3.8 and 5.6 with a warp each.  Where many
+// rows have 2 tiles a team's idle warps cost: 1024 rows of 512 2.3 and 2.8 us with
+// a warp each, 4.5 and 6.4 us with teams of 4 (taken).
 int team_for(long long rows, int L, int num_sms)
 {
     const long long tiles = ((long long)L + kScanTile - 1) / kScanTile;
@@ -1553,7 +1562,9 @@ cudaError_t step_launch(const void* v, const void* g, const float* h, void* y, f
                         long long rows, const Launch& L)
 {
     // 8 rows a thread once that leaves an SM two blocks of threads, where the
-    // buffers allow it: 256 x 8192 bf16 rows take 17.9 us one a thread
+    // buffers allow it: 256 x 8192 bf16 rows take 6.3 us (17.9 one a thread), fp32
+    // ones 10.8 us.  A thread's 32 bytes of an fp32 array (the states; in fp32 all
+    // five) are two accesses 32 bytes apart, each half of every sector
     uintptr_t all = 0;
     for (const void* p : {v, g, (const void*)h, (const void*)y, (const void*)h_next})
         all |= reinterpret_cast<uintptr_t>(p);
