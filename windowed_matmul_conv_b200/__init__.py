@@ -209,7 +209,8 @@ def _map_shape(x):
 
 def _windows(B, C, H, W, w):
     w = int(w)
-    _ints(w)
+    if w > _INT_MAX or w < -_INT_MAX:
+        _ints(w)
     return B * C * (H // w) * (W // w) if w > 0 else 0
 
 
@@ -219,7 +220,8 @@ def _seq_shape(v):
         raise ValueError("recurrence tensors must be [B, C, L], [B, C, H, W] or [B, C]")
     B, C = shape[0], shape[1]
     L = shape[2] if len(shape) == 3 else math.prod(shape[2:])
-    _ints(B, C, L)
+    if L > _INT_MAX or B > _INT_MAX or C > _INT_MAX:     # inline: the step's host time
+        _ints(B, C, L)
     return B, C, L
 
 
