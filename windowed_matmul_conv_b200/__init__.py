@@ -542,9 +542,11 @@ def checkpoint_restore(codes, exps, shape, w, dtype, stream=None):
     if stream is not None:
         return _on(stream, codes, checkpoint_restore, codes, exps, shape, w, dtype)
     B, C, H, W = shape
-    _ints(B, C, H, W)
+    n = B * C * H * W
+    if n > _INT_MAX:
+        _ints(B, C, H, W)
     x = codes.new_empty(shape, dtype=dtype)
-    _need("codes", codes, B * C * H * W, x, torch.uint8)
+    _need("codes", codes, n, x, torch.uint8)
     _need("exps", exps, _windows(B, C, H, W, w), x, torch.uint8)
     pc, pe = _ptrs(codes, exps)
     _check(_lib.wbmm_checkpoint_restore(pc, pe, x.data_ptr(), B, C, H, W, int(w), _dt(x),
