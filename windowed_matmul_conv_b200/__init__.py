@@ -444,7 +444,8 @@ def _on(stream, ref, call, *args, **kw):
     """A convenience call on a given stream.  What it allocates has to come from
     that stream's memory: the current stream's may still be in use there, and a
     workspace freed to it would be handed out while the kernels run."""
-    _p(ref), _stream(stream, ref)
+    _p(ref)                     # refused as by a call without a stream
+    _stream(stream, ref)
     with torch.cuda.stream(stream):
         return call(*args, **kw)
 
